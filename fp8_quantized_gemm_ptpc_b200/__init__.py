@@ -14,6 +14,7 @@ challenge: two-step vs fused".
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -68,6 +69,12 @@ SIGNATURES = {
     "ptpc_decode_attention_kernel": (ctypes.c_int, [_I64, _I64, _I64, _I64]),
     "ptpc_decode_attention": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
                                              _I64, _I64, ctypes.c_float, _P, _P, _SZ, _P]),
+    "ptpc_residual_norm": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, ctypes.c_float,
+                                          ctypes.c_float, _P, _I64, _P, _P]),
+    "ptpc_residual_norm_quantize": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, ctypes.c_float,
+                                                   ctypes.c_float, _P, _I64, _P, _P, _P]),
+    "ptpc_rope_kv_cache_append": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, ctypes.c_int, _P, _P,
+                                                 _I64, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P]),
     "ptpc_act_row_amax": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P]),
     "ptpc_quantize_activations_amax": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P, _P]),
     "ptpc_quantize_weights_fmt": (ctypes.c_int, [_P, _I64, _I64, ctypes.c_int, _P, _P, _P, _SZ, _P]),
@@ -301,6 +308,103 @@ def quantize_activations_amax(X: torch.Tensor, amax: torch.Tensor, Xq: torch.Ten
            lib.ptpc_quantize_activations_amax(_ptr(X), T, Ci, ldx, _ptr(amax), _ptr(Xq), _ptr(x_scale),
                                               _stream(X.device)))
     return Xq, x_scale
+
+
+def _on_device(fn):
+    """Runs an entry point with the device of its first tensor current (the
+    launch goes to the current device; the stream is already that device's)."""
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        dev = next((a.device for a in args if isinstance(a, torch.Tensor)), None)
+        if dev is None or not dev.type == "cuda" or dev.index == torch.cuda.current_device():
+            return fn(*args, **kwargs)
+        with torch.cuda.device(dev):
+            return fn(*args, **kwargs)
+    return call
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _norm_args(y, residual, pre_weight, post_weight, gate, h_out):
+    ldr = _need_rows(residual, "residual")
+    T, C = residual.shape
+    ldy = 0
+    if y is not None:
+        ldy = _need_rows(y, "y")
+        if y.shape != residual.shape:
+            raise ValueError("y and residual differ in shape")
+    for name, w in (("pre_weight", pre_weight), ("post_weight", post_weight)):
+        if w is not None or name == "pre_weight":
+            _need(w, name, torch.bfloat16, 1)
+            if w.shape[0] != C:
+                raise ValueError(f"{name} must have {C} values")
+    ldg = 0
+    if gate is not None:
+        if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+            _need(gate, "gate", torch.bfloat16, 1)
+            if gate.shape[0] != C:
+                raise ValueError(f"gate must have {C} values")
+        else:
+            ldg = _need_rows(gate, "gate")
+            if gate.shape != residual.shape:
+                raise ValueError("gate must be [C] or the shape of residual")
+    if h_out is None:
+        h_out = torch.empty((T, C), dtype=torch.bfloat16, device=residual.device)
+    ldh = _need_rows(h_out, "h_out")
+    if h_out.shape != residual.shape:
+        raise ValueError("h_out and residual differ in shape")
+    _same_device(residual.device, y=y, pre_weight=pre_weight, post_weight=post_weight, gate=gate, h_out=h_out)
+    opt = lambda t: None if t is None else _ptr(t)  # noqa: E731
+    return h_out, (opt(y), ldy, _ptr(residual), ldr, opt(gate), ldg, opt(post_weight), _ptr(pre_weight), T, C), ldh
+
+
+@_on_device
+def residual_norm(y, residual, pre_weight, post_weight=None, gate=None, residual_scale: float = 1.0,
+                  eps: float = 1e-5, h_out: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """The norms on either side of a residual add -> (h bf16 [T, C], x bf16 [T, C]):
+
+        u = y [* post_weight * rsqrt(mean(y^2) + eps)] [* gate]
+        h = residual + residual_scale * u
+        x = h * pre_weight * rsqrt(mean(h^2) + eps)
+
+    in fp32, each output rounded once.  y and residual bf16 [T, C] (rows
+    contiguous); weights bf16 [C]; gate bf16 [C] or [T, C].  y None: h is the
+    residual (the first norm of a model).  h_out may be residual itself."""
+    h_out, args, ldh = _norm_args(y, residual, pre_weight, post_weight, gate, h_out)
+    out = torch.empty(residual.shape, dtype=torch.bfloat16, device=residual.device) if out is None else out
+    _need(out, "out", torch.bfloat16, 2)
+    if out.shape != residual.shape:
+        raise ValueError("out and residual differ in shape")
+    _same_device(residual.device, out=out)
+    _check("ptpc_residual_norm",
+           lib.ptpc_residual_norm(*args, float(eps), float(residual_scale), _ptr(h_out), ldh, _ptr(out),
+                                  _stream(residual.device)))
+    return h_out, out
+
+
+@_on_device
+def residual_norm_quantize(y, residual, pre_weight, post_weight=None, gate=None, residual_scale: float = 1.0,
+                           eps: float = 1e-5, h_out: torch.Tensor | None = None, Xq: torch.Tensor | None = None,
+                           x_scale: torch.Tensor | None = None):
+    """residual_norm with x as the per-token E4M3 codes and scales that
+    scaled_mm reads -> (h bf16 [T, C], Xq uint8 [T, C], x_scale fp32 [T])."""
+    h_out, args, ldh = _norm_args(y, residual, pre_weight, post_weight, gate, h_out)
+    T, C = residual.shape
+    Xq = torch.empty((T, C), dtype=torch.uint8, device=residual.device) if Xq is None else Xq
+    x_scale = torch.empty((T,), dtype=torch.float32, device=residual.device) if x_scale is None else x_scale
+    _need(Xq, "Xq", torch.uint8, 2)
+    _need(x_scale, "x_scale", torch.float32, 1)
+    if Xq.shape != residual.shape or x_scale.shape[0] != T:
+        raise ValueError("Xq or x_scale does not fit residual")
+    _same_device(residual.device, Xq=Xq, x_scale=x_scale)
+    _check("ptpc_residual_norm_quantize",
+           lib.ptpc_residual_norm_quantize(*args, float(eps), float(residual_scale), _ptr(h_out), ldh, _ptr(Xq),
+                                           _ptr(x_scale), _stream(residual.device)))
+    return h_out, Xq, x_scale
 
 
 def quantize_weights(W: torch.Tensor, ws: Workspace | None = None):
@@ -591,6 +695,65 @@ def kv_cache_append(K, V, slots, k_cache, v_cache, k_scale, v_scale):
     _check("ptpc_kv_cache_append",
            lib.ptpc_kv_cache_append(_ptr(K), _ptr(V), _ptr(slots), T, H, D, bs, nb, _ptr(k_cache), _ptr(v_cache),
                                     _ptr(k_scale), _ptr(v_scale), _stream(K.device)))
+
+
+def _need_heads(t: torch.Tensor, name: str) -> int:
+    """A bf16 [T, H, D] tensor whose tokens' heads are dense (a dense tensor or
+    a slice of a fused projection's output); returns the token pitch in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be a 3-d tensor with dense heads")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _need_cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks the four tensors of a paged cache; returns (num_blocks, block_size, H, D)."""
+    _need(k_cache, "k_cache", torch.uint8, 4)
+    _need(v_cache, "v_cache", torch.uint8, 4)
+    _need(k_scale, "k_scale", torch.float32, 3)
+    _need(v_scale, "v_scale", torch.float32, 3)
+    if v_cache.shape != k_cache.shape or k_scale.shape != k_cache.shape[:3] or v_scale.shape != k_scale.shape:
+        raise ValueError("shape mismatch")
+    return tuple(k_cache.shape)
+
+
+@_on_device
+def rope_kv_cache_append(q, k, v, cos_sin, positions, slots, k_cache, v_cache, k_scale, v_scale,
+                         q_out: torch.Tensor | None = None, interleaved: bool = False) -> torch.Tensor:
+    """Turn q and k by their positions, quantise k and v and write them to
+    their slots of the paged cache -> q_out bf16 [T, Hq, D].
+
+    q bf16 [T, Hq, D], k and v bf16 [T, Hkv, D] (heads dense; slices of a
+    fused projection's output are fine); cos_sin fp32 [max_position, R]: R / 2
+    cosines, then R / 2 sines, for each position, R <= D the number of values
+    that turn; positions int64 [T]; slots and the cache as for
+    kv_cache_append.  Pairs are (i, i + R / 2), or (2i, 2i + 1) when
+    interleaved.  q_out may be q.  Of a token whose position is outside the
+    table nothing is written (a fresh q_out is then undefined there)."""
+    ldq, ldk, ldv = _need_heads(q, "q"), _need_heads(k, "k"), _need_heads(v, "v")
+    _need(cos_sin, "cos_sin", torch.float32, 2)
+    _need(positions, "positions", torch.int64, 1)
+    _need(slots, "slots", torch.int64, 1)
+    nb, bs, Hkv, D = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    T, Hq, _ = q.shape
+    if q.shape[2] != D or k.shape != (T, Hkv, D) or v.shape != k.shape or positions.shape[0] != T or \
+            slots.shape[0] != T:
+        raise ValueError("shape mismatch")
+    q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
+    ldo = _need_heads(q_out, "q_out")
+    if q_out.shape != q.shape:
+        raise ValueError("q_out and q differ in shape")
+    _same_device(q.device, k=k, v=v, cos_sin=cos_sin, positions=positions, slots=slots, k_cache=k_cache,
+                 v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, q_out=q_out)
+    _check("ptpc_rope_kv_cache_append",
+           lib.ptpc_rope_kv_cache_append(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(cos_sin), cos_sin.shape[0],
+                                         cos_sin.shape[1], int(bool(interleaved)), _ptr(positions), _ptr(slots), T,
+                                         Hq, Hkv, D, bs, nb, _ptr(q_out), ldo, _ptr(k_cache), _ptr(v_cache),
+                                         _ptr(k_scale), _ptr(v_scale), _stream(q.device)))
+    return q_out
 
 
 def decode_attention_kernel(Hq: int, Hkv: int, D: int, block_size: int) -> str:

@@ -1,5 +1,6 @@
 // C ABI of the PTPC-FP8 library: argument checks, workspace layout and
 // dispatch to the sm_100a kernels.  Declared in include/ptpc.h.
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -179,6 +180,62 @@ int ptpc_quantize_activations_amax(const void *X, int64_t T, int64_t Ci, int64_t
       ptpc::launch_quant_act_amax(X, (int)T, (int)Ci, ldx, amax, Xq, x_scale, (cudaStream_t)stream));
 }
 
+namespace {
+int run_residual_norm(const void *y, int64_t ldy, const void *residual, int64_t ldr, const void *gate, int64_t ldg,
+                      const void *post_w, const void *pre_w, int64_t T, int64_t C, float eps, float residual_scale,
+                      void *h, int64_t ldh, void *x, uint8_t *Xq, float *x_scale, bool quant, void *stream) {
+  int s = check_shape_tci(T, C);
+  if (s != PTPC_OK) return s;
+  if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(residual_scale)) return PTPC_ERR_INVALID_ARG;
+  if (T == 0) return PTPC_OK;
+  if (!residual || !pre_w || (quant ? !Xq || !x_scale : !x)) return PTPC_ERR_INVALID_ARG;
+  if (!y && (gate || post_w)) return PTPC_ERR_INVALID_ARG;
+  if ((s = check_ldx(ldr, C)) != PTPC_OK) return s;
+  if (y && (s = check_ldx(ldy, C)) != PTPC_OK) return s;
+  if (gate && ldg != 0 && (s = check_ldx(ldg, C)) != PTPC_OK) return s;
+  if (h && (s = check_ldx(ldh, C)) != PTPC_OK) return s;
+  if (h == residual && ldh != ldr) return PTPC_ERR_INVALID_ARG;
+  if (!aligned16(y) || !aligned16(residual) || !aligned16(gate) || !aligned16(post_w) || !aligned16(pre_w) ||
+      !aligned16(h) || !aligned16(x) || !aligned16(Xq) || !aligned16(x_scale))
+    return PTPC_ERR_MISALIGNED;
+  if ((s = check_device()) != PTPC_OK) return s;
+  ptpc::ResidualNorm p{};
+  p.y = y;
+  p.residual = residual;
+  p.gate = gate;
+  p.post_w = post_w;
+  p.pre_w = pre_w;
+  p.ldy = ldy;
+  p.ldr = ldr;
+  p.ldg = ldg;
+  p.ldh = ldh;
+  p.T = (int)T;
+  p.C = (int)C;
+  p.eps = eps;
+  p.residual_scale = residual_scale;
+  p.h = h;
+  p.x = x;
+  p.xq = Xq;
+  p.xs = x_scale;
+  return cuda_status(ptpc::launch_residual_norm(p, (cudaStream_t)stream));
+}
+}  // namespace
+
+int ptpc_residual_norm(const void *y, int64_t ldy, const void *residual, int64_t ldr, const void *gate, int64_t ldg,
+                       const void *post_w, const void *pre_w, int64_t T, int64_t C, float eps, float residual_scale,
+                       void *h, int64_t ldh, void *x, void *stream) {
+  return run_residual_norm(y, ldy, residual, ldr, gate, ldg, post_w, pre_w, T, C, eps, residual_scale, h, ldh, x,
+                           nullptr, nullptr, false, stream);
+}
+
+int ptpc_residual_norm_quantize(const void *y, int64_t ldy, const void *residual, int64_t ldr, const void *gate,
+                                int64_t ldg, const void *post_w, const void *pre_w, int64_t T, int64_t C, float eps,
+                                float residual_scale, void *h, int64_t ldh, uint8_t *Xq, float *x_scale,
+                                void *stream) {
+  return run_residual_norm(y, ldy, residual, ldr, gate, ldg, post_w, pre_w, T, C, eps, residual_scale, h, ldh, nullptr,
+                           Xq, x_scale, true, stream);
+}
+
 int ptpc_quantize_weights(const void *W, int64_t Ci, int64_t Co, uint8_t *Wq_t, float *w_scale, void *ws,
                           size_t ws_bytes, void *stream) {
   int s = check_shape_tci(0, Ci);
@@ -333,6 +390,57 @@ int ptpc_kv_cache_append(const void *K, const void *V, const int64_t *slots, int
   if ((s = check_device()) != PTPC_OK) return s;
   return cuda_status(ptpc::launch_kv_append(K, V, slots, (int)T, (int)H, (int)D, num_blocks * block_size, k_cache,
                                             v_cache, k_scale, v_scale, (cudaStream_t)stream));
+}
+
+int ptpc_rope_kv_cache_append(const void *Q, int64_t ldq, const void *K, int64_t ldk, const void *V, int64_t ldv,
+                              const float *cos_sin, int64_t max_position, int64_t rotary_dim, int interleaved,
+                              const int64_t *positions, const int64_t *slots, int64_t T, int64_t Hq, int64_t Hkv,
+                              int64_t D, int64_t block_size, int64_t num_blocks, void *Q_out, int64_t ldo,
+                              uint8_t *k_cache, uint8_t *v_cache, float *k_scale, float *v_scale, void *stream) {
+  int s = check_kv_dims(Hkv, D, block_size, num_blocks);
+  if (s != PTPC_OK) return s;
+  if (T < 0 || Hq < 0 || max_position <= 0 || rotary_dim <= 0) return PTPC_ERR_INVALID_ARG;
+  if (T > kMaxDim || Hq > 16384 || max_position > kMaxDim || num_blocks > kMaxDim / block_size ||
+      rotary_dim % 16 != 0 || rotary_dim > D)
+    return PTPC_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return PTPC_OK;
+  if (!K || !V || !cos_sin || !positions || !slots || !k_cache || !v_cache || !k_scale || !v_scale ||
+      (Hq > 0 && (!Q || !Q_out)))
+    return PTPC_ERR_INVALID_ARG;
+  if ((s = check_ldx(ldk, Hkv * D)) != PTPC_OK || (s = check_ldx(ldv, Hkv * D)) != PTPC_OK) return s;
+  if (Hq > 0 && ((s = check_ldx(ldq, Hq * D)) != PTPC_OK || (s = check_ldx(ldo, Hq * D)) != PTPC_OK)) return s;
+  if (Hq > 0 && Q == Q_out && ldq != ldo) return PTPC_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(cos_sin) || !aligned16(Q_out) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || (reinterpret_cast<uintptr_t>(positions) & 7u) ||
+      (reinterpret_cast<uintptr_t>(slots) & 7u) || (reinterpret_cast<uintptr_t>(k_scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(v_scale) & 3u))
+    return PTPC_ERR_MISALIGNED;
+  if ((s = check_device()) != PTPC_OK) return s;
+  ptpc::RopeAppend p{};
+  p.q = Q;
+  p.k = K;
+  p.v = V;
+  p.ldq = ldq;
+  p.ldk = ldk;
+  p.ldv = ldv;
+  p.ldo = ldo;
+  p.cos_sin = cos_sin;
+  p.max_position = max_position;
+  p.rot = (int)rotary_dim;
+  p.interleaved = interleaved != 0;
+  p.positions = positions;
+  p.slots = slots;
+  p.T = (int)T;
+  p.Hq = (int)Hq;
+  p.Hkv = (int)Hkv;
+  p.D = (int)D;
+  p.num_slots = num_blocks * block_size;
+  p.q_out = Q_out;
+  p.kc = k_cache;
+  p.vc = v_cache;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  return cuda_status(ptpc::launch_rope_append(p, (cudaStream_t)stream));
 }
 
 size_t ptpc_decode_attention_workspace_size(int64_t B, int64_t Hq, int64_t D, int64_t max_context) {

@@ -87,4 +87,56 @@ void map_cache_stats(uint64_t *hits, uint64_t *misses);
 // GPU needed): number of failed checks, 0 when it behaves.
 int map_cache_selftest();
 
+// Launch with programmatic stream serialisation: the kernel may be scheduled
+// while the previous kernel in the stream finishes, and waits for it with
+// griddepcontrol.wait before touching global memory.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int block, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = 0;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// Residual add and norms (norm.cu).  Pitches are in elements (multiples of
+// 8); y, gate, post_w and h may be null (ldg == 0: one gate row for every
+// token).  Exactly one of x (bf16 [T, C]) and xq (codes [T, C], with scales
+// xs [T]) is written.
+struct ResidualNorm {
+  const void *y, *residual, *gate, *post_w, *pre_w;
+  int64_t ldy, ldr, ldg, ldh;
+  int T, C;
+  float eps, residual_scale;
+  void *h, *x;
+  uint8_t *xq;
+  float *xs;
+};
+cudaError_t launch_residual_norm(const ResidualNorm &p, cudaStream_t st);
+
+// Rotation of queries and keys, and the append of keys and values to the FP8
+// cache (rope_append.cu).  Pitches in elements (multiples of 8); q may be
+// null (Hq == 0).
+struct RopeAppend {
+  const void *q, *k, *v;
+  int64_t ldq, ldk, ldv, ldo;
+  const float *cos_sin;        // [max_position, rot]
+  int64_t max_position;
+  int rot;
+  bool interleaved;
+  const int64_t *positions, *slots;
+  int T, Hq, Hkv, D;
+  int64_t num_slots;
+  void *q_out;
+  uint8_t *kc, *vc;
+  float *ks, *vs;
+};
+cudaError_t launch_rope_append(const RopeAppend &p, cudaStream_t st);
+
 }  // namespace ptpc

@@ -134,6 +134,38 @@ PTPC_API int ptpc_quantize_activations_amax(const void *X_dev, int64_t T, int64_
                                             const float *amax_dev, uint8_t *Xq_dev, float *x_scale_dev,
                                             void *stream);
 
+/* The norms on either side of a residual add, fused with it.  For each token t
+ * (fp32 throughout, each output rounded once):
+ *   u = y[t]                                   (h = residual[t] alone where y_dev is NULL)
+ *   u = (u * post_w) * rsqrt(mean(u^2) + eps)  (skipped where post_w_dev is NULL)
+ *   u = u * gate                               (skipped where gate_dev is NULL)
+ *   h = residual[t] + residual_scale * u
+ *   x = (h * pre_w) * rsqrt(mean(h^2) + eps)
+ *   y_dev, residual_dev  bf16 [T, C] with row pitches ldy, ldr (as ldx above);
+ *   gate_dev     bf16, row pitch ldg: 0 for one row [C] that every token uses,
+ *                else a row a token (ldg >= C, ldg % 8 == 0);
+ *   post_w_dev, pre_w_dev  bf16 [C];
+ *   h_dev        bf16 [T, C], row pitch ldh: the rounded h.  NULL: not written.  It may
+ *                be residual_dev itself (ldh == ldr); no other output may overlap an input.
+ *   x_dev        bf16 [T, C] dense: the rounded x.
+ * C is a positive multiple of 16; eps > 0 and residual_scale finite
+ * (PTPC_ERR_INVALID_ARG); post_w_dev and gate_dev need y_dev. */
+PTPC_API int ptpc_residual_norm(const void *y_dev, int64_t ldy, const void *residual_dev, int64_t ldr,
+                                const void *gate_dev, int64_t ldg, const void *post_w_dev, const void *pre_w_dev,
+                                int64_t T, int64_t C, float eps, float residual_scale, void *h_dev, int64_t ldh,
+                                void *x_dev, void *stream);
+
+/* The same with x leaving as the per-token codes and scales of
+ * ptpc_quantize_activations, taken from the fp32 x (not from its bf16
+ * rounding), ready for ptpc_scaled_mm: x_scale[t] = amax|x| / 448 (1.0f and
+ * all codes 0x00 where that is 0), Xq = E4M3_satRNE(x / x_scale[t]).
+ *   Xq_dev u8 [T, C] dense, x_scale_dev fp32 [T]. */
+PTPC_API int ptpc_residual_norm_quantize(const void *y_dev, int64_t ldy, const void *residual_dev, int64_t ldr,
+                                         const void *gate_dev, int64_t ldg, const void *post_w_dev,
+                                         const void *pre_w_dev, int64_t T, int64_t C, float eps,
+                                         float residual_scale, void *h_dev, int64_t ldh, uint8_t *Xq_dev,
+                                         float *x_scale_dev, void *stream);
+
 /* Per-output-channel weight quantisation (the page's Delta_W[1 x Co]); run
  * once per weight, e.g. when a bf16 checkpoint is loaded.
  *   W_dev       bf16 [Ci, Co] row-major, read only.
@@ -342,6 +374,30 @@ PTPC_API int ptpc_kv_cache_append(const void *K_dev, const void *V_dev, const in
                                   int64_t H, int64_t D, int64_t block_size, int64_t num_blocks,
                                   uint8_t *k_cache_dev, uint8_t *v_cache_dev, float *k_scale_dev,
                                   float *v_scale_dev, void *stream);
+
+/* ptpc_kv_cache_append with the rotary position embedding applied on the way,
+ * to the queries too.  The first rotary_dim values of every head of Q and K
+ * are turned in pairs (a, b) by their token's angles:
+ *   (a, b) -> (a c - b s, b c + a s),   each product and each sum rounded to fp32,
+ * the pairs being (i, i + rotary_dim / 2), or (2i, 2i + 1) with interleaved != 0,
+ * i < rotary_dim / 2, c = cos_sin[pos][i], s = cos_sin[pos][rotary_dim / 2 + i].
+ * Q leaves as bf16; K, from the fp32 values, and V are quantised and written
+ * as ptpc_kv_cache_append does.
+ *   Q_dev  bf16 [T, Hq, D], token pitch ldq elements (ldq >= Hq * D, ldq % 8 == 0; heads are
+ *          dense: e.g. a column slice of a fused projection's output).  Hq == 0: none.
+ *   K_dev, V_dev  bf16 [T, Hkv, D], token pitches ldk, ldv;
+ *   cos_sin_dev   fp32 [max_position, rotary_dim]; rotary_dim a multiple of 16, at most D;
+ *   positions_dev int64 [T]: of a token whose position is negative or >= max_position
+ *          nothing is written, neither to Q_out nor to the cache;
+ *   slots_dev     int64 [T]: as for ptpc_kv_cache_append (a skipped slot's query is still turned);
+ *   Q_out_dev     bf16 [T, Hq, D], token pitch ldo; it may be Q_dev itself (ldo == ldq). */
+PTPC_API int ptpc_rope_kv_cache_append(const void *Q_dev, int64_t ldq, const void *K_dev, int64_t ldk,
+                                       const void *V_dev, int64_t ldv, const float *cos_sin_dev,
+                                       int64_t max_position, int64_t rotary_dim, int interleaved,
+                                       const int64_t *positions_dev, const int64_t *slots_dev, int64_t T, int64_t Hq,
+                                       int64_t Hkv, int64_t D, int64_t block_size, int64_t num_blocks,
+                                       void *Q_out_dev, int64_t ldo, uint8_t *k_cache_dev, uint8_t *v_cache_dev,
+                                       float *k_scale_dev, float *v_scale_dev, void *stream);
 
 /* Workspace bytes of ptpc_decode_attention (0 on invalid arguments): the
  * device status word (first 256 bytes) and the chunks' partial results. */
