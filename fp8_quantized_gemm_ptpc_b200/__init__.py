@@ -75,6 +75,10 @@ SIGNATURES = {
                                                    ctypes.c_float, _P, _I64, _P, _P, _P]),
     "ptpc_rope_kv_cache_append": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, ctypes.c_int, _P, _P,
                                                  _I64, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P]),
+    "ptpc_chunk_attention_workspace_size": (ctypes.c_size_t, [_I64] * 7),
+    "ptpc_chunk_attention_splits": (ctypes.c_int, [_I64] * 7),
+    "ptpc_chunk_attention": (ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _P, _P, _P] + [_I64] * 10 +
+                             [ctypes.c_float, _P, _P, _SZ, _P]),
     "ptpc_act_row_amax": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P]),
     "ptpc_quantize_activations_amax": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P, _P]),
     "ptpc_quantize_weights_fmt": (ctypes.c_int, [_P, _I64, _I64, ctypes.c_int, _P, _P, _P, _SZ, _P]),
@@ -213,6 +217,16 @@ class Workspace:
     def __init__(self, nbytes: int, device):
         self.device = torch.device(device)
         self.buf = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
+
+    @classmethod
+    def status_only(cls, nbytes: int, device) -> "Workspace":
+        """A workspace of its own for an entry point that needs no more than
+        the status word (the first 256 bytes) zero-filled."""
+        ws = cls.__new__(cls)
+        ws.device = torch.device(device)
+        ws.buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=ws.device)
+        ws.buf[:256].zero_()
+        return ws
 
     @property
     def nbytes(self) -> int:
@@ -783,4 +797,54 @@ def decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, contex
                                      _ptr(block_tables), _ptr(context_lens), B, Hq, Hkv, D, bs, nb,
                                      block_tables.shape[1], max_context, float(softmax_scale), _ptr(out), ws.ptr(),
                                      ws.nbytes, _stream(q.device)))
+    return out
+
+
+def chunk_attention_splits(total_q: int, B: int, Hq: int, Hkv: int, D: int, max_q: int, max_context: int) -> int:
+    """The CTAs that share a context in chunk_attention's plan (1: none is split; 0: invalid or nothing to do)."""
+    return int(lib.ptpc_chunk_attention_splits(total_q, B, Hq, Hkv, D, max_q, max_context))
+
+
+@_on_device
+def chunk_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, cu_q, max_q: int,
+                    max_context: int, softmax_scale: float, out: torch.Tensor | None = None,
+                    ws: Workspace | None = None) -> torch.Tensor:
+    """Causal attention of each sequence's newest tokens over the FP8 paged
+    cache -> out bf16 [total_q, Hq, D].
+
+    q bf16 [total_q, Hq, D] (heads dense): the new tokens of the sequences one
+    behind the other, sequence b's at rows cu_q[b] .. cu_q[b + 1] - 1 (cu_q
+    int32 [B + 1]; at most max_q each); they are the last of its context of
+    context_lens[b] positions (int32 [B], at most max_context), which are in
+    the cache already; block_tables int32 [B, max_blocks].  A token sees the
+    positions up to its own.  Rows of no sequence are left as they were (a
+    fresh out is undefined there).  In a graph capture without ``ws`` the call
+    gets a workspace of its own from the capture's pool."""
+    ldq = _need_heads(q, "q")
+    nb, bs, Hkv, D = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    _need(cu_q, "cu_q", torch.int32, 1)
+    total, Hq, _ = q.shape
+    B = context_lens.shape[0]
+    if q.shape[2] != D or Hq % Hkv or block_tables.shape[0] != B or cu_q.shape[0] != B + 1:
+        raise ValueError("shape mismatch")
+    out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+    _need(out, "out", torch.bfloat16, 3)
+    if out.shape != q.shape:
+        raise ValueError("out and q differ in shape")
+    _same_device(q.device, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                 block_tables=block_tables, context_lens=context_lens, cu_q=cu_q, out=out)
+    need = int(lib.ptpc_chunk_attention_workspace_size(total, B, Hq, Hkv, D, max_q, max_context))
+    if ws is not None:
+        ws.ensure(need)
+    elif torch.cuda.is_current_stream_capturing():
+        ws = Workspace.status_only(need, q.device)
+    else:
+        ws = default_workspace(need, q.device)
+    _check("ptpc_chunk_attention",
+           lib.ptpc_chunk_attention(_ptr(q), ldq, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                    _ptr(block_tables), _ptr(context_lens), _ptr(cu_q), total, B, max_q, Hq, Hkv, D,
+                                    bs, nb, block_tables.shape[1], max_context, float(softmax_scale), _ptr(out),
+                                    ws.ptr(), ws.nbytes, _stream(q.device)))
     return out

@@ -22,7 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libptpc.so")
-SOURCES = ["api.cu", "gemm.cu", "quant.cu", "attention.cu", "attention_tc.cu", "norm.cu", "rope_append.cu",
+SOURCES = ["api.cu", "gemm.cu", "quant.cu", "attention.cu", "attention_tc.cu", "norm.cu", "rope_append.cu", "chunk_attention.cu",
            "bench_probe.cu"]
 HEADERS = ["sm100.cuh", "kernels.h", "quant_math.cuh", "attention_tc.h", "bench_probe.h"]
 

@@ -481,6 +481,84 @@ int ptpc_decode_attention_kernel(int64_t Hq, int64_t Hkv, int64_t D, int64_t blo
   return ptpc::attn_kernel_choice((int)D, (int)(Hq / Hkv), (int)block_size);
 }
 
+namespace {
+int check_chunk_shape(int64_t total_q, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q,
+                      int64_t max_context) {
+  if (total_q < 0 || B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_q < 0 || max_context < 0)
+    return PTPC_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || Hkv > 1024 || Hq % Hkv != 0 || Hq > 16384 || B > 65535 || total_q > kMaxDim / Hq ||
+      max_q > kMaxDim / Hq || max_context > kMaxDim - 256)
+    return PTPC_ERR_UNSUPPORTED_SHAPE;
+  if (total_q > 0 && B > 0 && max_q > 0 &&
+      ptpc::chunk_attn_ctas(total_q, B, (int)Hq, (int)Hkv, max_q, max_context) > kMaxDim)
+    return PTPC_ERR_UNSUPPORTED_SHAPE;
+  return PTPC_OK;
+}
+}  // namespace
+
+size_t ptpc_chunk_attention_workspace_size(int64_t total_q, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                           int64_t max_q, int64_t max_context) {
+  if (check_chunk_shape(total_q, B, Hq, Hkv, D, max_q, max_context) != PTPC_OK) return 0;
+  if (total_q == 0 || B == 0 || max_q == 0) return kAlign;
+  return round_up(ptpc::chunk_attn_workspace_bytes(total_q, B, (int)Hq, (int)Hkv, (int)D, max_q, max_context));
+}
+
+int ptpc_chunk_attention_splits(int64_t total_q, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q,
+                                int64_t max_context) {
+  if (check_chunk_shape(total_q, B, Hq, Hkv, D, max_q, max_context) != PTPC_OK) return 0;
+  if (total_q == 0 || B == 0 || max_q == 0) return 0;
+  return ptpc::chunk_attn_splits(total_q, B, (int)Hq, (int)Hkv, max_q, max_context);
+}
+
+int ptpc_chunk_attention(const void *q, int64_t ldq, const uint8_t *k_cache, const uint8_t *v_cache,
+                         const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                         const int32_t *context_lens, const int32_t *cu_q, int64_t total_q, int64_t B, int64_t max_q,
+                         int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size, int64_t num_blocks,
+                         int64_t max_blocks, int64_t max_context, float softmax_scale, void *out, void *ws,
+                         size_t ws_bytes, void *stream) {
+  int s = check_kv_dims(Hkv, D, block_size, num_blocks);
+  if (s != PTPC_OK) return s;
+  if ((s = check_chunk_shape(total_q, B, Hq, Hkv, D, max_q, max_context)) != PTPC_OK) return s;
+  if (max_blocks <= 0 || !(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return PTPC_ERR_INVALID_ARG;
+  if (max_blocks > kMaxDim / block_size || num_blocks > kMaxDim / block_size) return PTPC_ERR_UNSUPPORTED_SHAPE;
+  if (total_q == 0 || B == 0 || max_q == 0) return PTPC_OK;
+  if ((s = check_ldx(ldq, Hq * D)) != PTPC_OK) return s;
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !context_lens || !cu_q || !out || !ws)
+    return PTPC_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(ws) ||
+      (reinterpret_cast<uintptr_t>(k_scale) & 3u) || (reinterpret_cast<uintptr_t>(v_scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(cu_q) & 3u))
+    return PTPC_ERR_MISALIGNED;
+  if (ws_bytes < ptpc_chunk_attention_workspace_size(total_q, B, Hq, Hkv, D, max_q, max_context))
+    return PTPC_ERR_WORKSPACE_TOO_SMALL;
+  if ((s = check_device()) != PTPC_OK) return s;
+  ptpc::ChunkAttention p{};
+  p.q = q;
+  p.ldq = ldq;
+  p.kc = k_cache;
+  p.vc = v_cache;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.cu_q = cu_q;
+  p.B = (int)B;
+  p.total_q = (int)total_q;
+  p.max_q = (int)max_q;
+  p.Hq = (int)Hq;
+  p.Hkv = (int)Hkv;
+  p.D = (int)D;
+  p.block_size = (int)block_size;
+  p.max_blocks = (int)max_blocks;
+  p.max_context = (int)max_context;
+  p.num_slots = num_blocks * block_size;
+  p.softmax_scale = softmax_scale;
+  p.out = out;
+  p.ws = ws;
+  return cuda_status(ptpc::launch_chunk_attention(p, (cudaStream_t)stream));
+}
+
 int ptpc_gemm_ksplit(int64_t T, int64_t Ci, int64_t Co) {
   if (check_shape_tci(T, Ci) != PTPC_OK || check_co(Co) != PTPC_OK || T == 0) return 0;
   if (check_device() != PTPC_OK) return 0;

@@ -139,4 +139,25 @@ struct RopeAppend {
 };
 cudaError_t launch_rope_append(const RopeAppend &p, cudaStream_t st);
 
+// Causal attention of each sequence's newest tokens over its FP8 paged cache
+// (chunk_attention.cu).  ws: the device status word, then the partial results
+// of contexts split over CTAs (chunk_attn_workspace_bytes).
+struct ChunkAttention {
+  const void *q;
+  int64_t ldq;
+  const uint8_t *kc, *vc;
+  const float *ks, *vs;
+  const int32_t *block_tables, *context_lens, *cu_q;
+  int B, total_q, max_q, Hq, Hkv, D, block_size, max_blocks, max_context;
+  int64_t num_slots;
+  float softmax_scale;
+  void *out, *ws;
+};
+cudaError_t launch_chunk_attention(const ChunkAttention &p, cudaStream_t st);
+size_t chunk_attn_workspace_bytes(int64_t total_q, int64_t B, int Hq, int Hkv, int D, int64_t max_q,
+                                  int64_t max_context);
+// CTAs that share a context, and row tiles times KV heads, of a call's plan.
+int chunk_attn_splits(int64_t total_q, int64_t B, int Hq, int Hkv, int64_t max_q, int64_t max_context);
+int64_t chunk_attn_ctas(int64_t total_q, int64_t B, int Hq, int Hkv, int64_t max_q, int64_t max_context);
+
 }  // namespace ptpc

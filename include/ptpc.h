@@ -436,6 +436,52 @@ PTPC_API int ptpc_decode_attention(const void *q_dev, const uint8_t *k_cache_dev
                                    int64_t max_blocks, int64_t max_context, float softmax_scale, void *out_dev,
                                    void *ws_dev, size_t ws_bytes, void *stream);
 
+/* Workspace bytes of ptpc_chunk_attention (0 on invalid arguments): the device
+ * status word (first 256 bytes) and the partial results of contexts that are
+ * split over CTAs. */
+PTPC_API size_t ptpc_chunk_attention_workspace_size(int64_t total_q, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                                    int64_t max_q, int64_t max_context);
+
+/* Causal attention of each sequence's newest tokens over the FP8 cache (a
+ * chunk of a prompt, a whole prompt, drafted tokens, or one token): sequence b
+ * has n = cu_q[b+1] - cu_q[b] new tokens, the last of its context of
+ * context_lens[b] = m positions, all of them in the cache already
+ * (ptpc_rope_kv_cache_append).  Token i of them sees positions 0 .. m - n + i.
+ *   q_dev      bf16 [total_q, Hq, D], token pitch ldq elements (ldq >= Hq * D, ldq % 8 == 0;
+ *              heads dense): the sequences' tokens one behind the other, sequence b's at rows
+ *              cu_q[b] .. cu_q[b+1] - 1.  Query head h reads KV head h / (Hq / Hkv).
+ *   cu_q_dev   int32 [B + 1], not decreasing, cu_q[B] <= total_q.  Rows of q before cu_q[0] and
+ *              from cu_q[B] on (a padded batch) belong to no sequence: their rows of out are
+ *              left as they were.
+ *   block_tables_dev int32 [B, max_blocks], context_lens_dev int32 [B]: as for
+ *              ptpc_decode_attention (context_lens <= max_context; positions whose entry is
+ *              missing, negative or past the cache are left out).
+ *   max_q      at least every sequence's number of new tokens (a bound; it sizes the launch).
+ *   softmax_scale  finite and > 0 (PTPC_ERR_INVALID_ARG).
+ *   out_dev    bf16 [total_q, Hq, D] dense:
+ *              bf16_RNE(sum_l p_l * v_scale_l * dec(V_l[d])),
+ *              p = softmax_l(softmax_scale * k_scale_l * sum_d q[d] * dec(K_l[d]));
+ *              0 for a token that sees no position (m < n, or no block in the table).
+ *   ws_dev     ptpc_chunk_attention_workspace_size(...) bytes; its first word must be zero
+ *              before the first call and is the device status word (ptpc_get_device_status).
+ * The products run on the tensor cores in f16 with fp32 accumulation: keys and
+ * values enter as code * scale / (a scale of 32 positions), rounded to f16's 11
+ * bits, weights as f16, statistics and sums are fp32.  Results do not depend
+ * on the other sequences of the call as long as the plan (below) is the same. */
+PTPC_API int ptpc_chunk_attention(const void *q_dev, int64_t ldq, const uint8_t *k_cache_dev,
+                                  const uint8_t *v_cache_dev, const float *k_scale_dev, const float *v_scale_dev,
+                                  const int32_t *block_tables_dev, const int32_t *context_lens_dev,
+                                  const int32_t *cu_q_dev, int64_t total_q, int64_t B, int64_t max_q, int64_t Hq,
+                                  int64_t Hkv, int64_t D, int64_t block_size, int64_t num_blocks, int64_t max_blocks,
+                                  int64_t max_context, float softmax_scale, void *out_dev, void *ws_dev,
+                                  size_t ws_bytes, void *stream);
+
+/* The CTAs that share a context in ptpc_chunk_attention's plan for these sizes
+ * (1: none is split; 0 on invalid arguments or nothing to do).  Launches
+ * nothing. */
+PTPC_API int ptpc_chunk_attention_splits(int64_t total_q, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q,
+                                         int64_t max_context);
+
 /* Which decode-attention kernel ptpc_decode_attention runs for a shape on
  * this library: 2 the kernel on the fifth-generation tensor cores (tcgen05
  * MMAs into tensor memory, TMA loads), for D = 128 and block sizes that are
