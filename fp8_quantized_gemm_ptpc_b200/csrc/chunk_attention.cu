@@ -8,18 +8,18 @@
 // and walks the context in tiles of 128 positions with the running maximum and
 // sum of a softmax.
 //
-// Warps 8-11 read the codes (16 bytes a lane; any block size; a tile ahead, in
-// registers), turn them into f16 and lay them out in shared memory for the
-// MMAs.  The scales go in here, relative to a reference of each 32 positions
+// Warps 8-11 (K) and 12-15 (V) read the codes (16 bytes a lane; any block size;
+// a tile ahead, in registers), turn them into f16 and lay them out in shared
+// memory for the MMAs.  The scales go in here, relative to a reference of each 32 positions
 // (a warp's rows):  K' = code * ks / kref,  V' = code * vs / vref, so that the
-// softmax has one factor for 32 columns instead of one a column.  kref is the
-// largest key scale; the product is formed as code * hi + code * lo with the
-// ratio split in two f16, so K' is rounded once.  vref is 2^-6 of a power of
-// two at least the largest value scale: V' reaches 448 * 64, near f16's largest
+// softmax has one factor for 32 columns instead of one a column.  kref is a
+// power of two at least the largest key scale; the product is formed as code *
+// hi + code * lo with the ratio split in two f16, so K' is rounded once.  vref
+// is 2^-6 of such a power for the value scales: V' reaches 448 * 64, near f16's largest
 // value, so that the ratio keeps f16's 11 bits down to 2^-20 of the largest
 // scale.  A key's error is 2^-12 of its value, spread over D products; a
 // value's at most 2^-11.
-// Warp 12 issues S = Q K'^T (kind::f16, q as f16 after a power-of-two scale a
+// Warps 16 and 17 (a stream each) issue S = Q K'^T (kind::f16, q as f16 after a power-of-two scale a
 // row, exact) and O += P V' with P from tensor memory.
 // Warps 0-3 and 4-7 (a stream each, a thread a row) do the softmax in base 2.
 // With t = S * kref * qscale * log2 e, a weight is P' = 2^(t + log2 vref - r):
@@ -49,7 +49,12 @@ namespace ptpc {
 
 namespace {
 
-constexpr int kCaThreads = 416;   // warps 0-7 softmax, 8-11 converters, 12 MMA issuer
+// Warpgroups: 0, 1 the softmax of a stream each, 2 converts K, 3 converts V,
+// 4 issues the products (its first two warps, a stream each).
+constexpr int kCaThreads = 640;
+// Registers a thread once the roles part (the softmax keeps a row's 128
+// scores): 2 x 160 + 2 x 64 + 32 = 5 x 96, what the CTA is launched with.
+constexpr int kCaRegsSoftmax = 160, kCaRegsConvert = 64, kCaRegsIssuer = 32;
 constexpr int kCaRows = 128;      // rows a stream
 constexpr int kCaTile = 128;      // positions a tile
 constexpr int kCaStages = 2;      // stages of the K ring and of the V ring
@@ -94,7 +99,7 @@ struct CaSmem {
   static constexpr int META = V + kCaStages * kOperand;
   static constexpr int ML = META + kCaMeta * (int)sizeof(TileMeta);  // [row]: r and l of stream 1 when joined
   static constexpr int BARS = ML + kCaRows * 8;
-  static constexpr int kBars = 4 * kCaStages + 3 * 2 + 1;
+  static constexpr int kBars = 4 * kCaStages + 4 * 2 + 3;
   static constexpr int BYTES = 1024 + BARS + kBars * 8 + 16;
 };
 
@@ -152,20 +157,37 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
   return r;
 }
 
+// The upper halves of the operands' shared-memory descriptors; the lower half
+// is (address >> 4) | (byte offset between atoms along M or N >> 4) << 16, and
+// a step inside a tile adds to it, so the issuing thread spends an addition a
+// product.
+constexpr uint32_t kDescHi = (1024u >> 4)    // 8-row atoms 1024 bytes apart
+                             | 1u << 14      // descriptor version (tcgen05)
+                             | 2u << 29;     // 128-byte swizzle
+// K-major tile: rows of 64 f16 along K (128 bytes).
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4 | 1u << 16; }
+// MN-major tile: rows of 64 f16 along N, one per K index; the next 64 values
+// of N start kCaRows * 128 bytes further.
+__device__ __forceinline__ uint32_t desc_mn_major(uint32_t saddr) {
+  return (saddr & 0x3FFFFu) >> 4 | (uint32_t)(kCaRows * 128 >> 4) << 16;
+}
+
 // D[tmem] (+)= A[smem] * B[smem], kind::f16 -> fp32.
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+template <bool ACC>
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "n"(ACC ? 1 : 0)
       : "memory");
 }
 // The same with A in tensor memory (two f16 along K a column, a row a lane).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(acc)
       : "memory");
 }
 
@@ -178,23 +200,38 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 
+// Loads that stay where they are written, so that a tile's are in flight
+// while the tile before it is converted.
+__device__ __forceinline__ uint4 ld_codes(const uint8_t *ptr) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(ptr));
+  return v;
+}
+__device__ __forceinline__ float ld_scale(const float *ptr) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(ptr));
+  return v;
+}
+
+// Ties loaded registers to the wait before: nothing that reads them moves above it.
+__device__ __forceinline__ void arrived32(uint32_t (&r)[32]) {
+  #pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                 "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // Instruction descriptor: dense kind::f16, f16 operands, fp32 accumulation,
 // M = 128; B K-major, or MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kCaRows >> 4) << 24);
-}
-
-// MN-major operand with the 128-byte swizzle: rows of 128 bytes (64 f16 along
-// N), one per K index, 8-row atoms 1024 bytes apart along K; the next 64
-// values of N start `atom_bytes` further.
-__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t atom_bytes) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(atom_bytes >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
 }
 
 // Byte offset of 16-byte piece c (0 .. D / 8 - 1) of row r in an operand tile:
@@ -266,10 +303,11 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
   uint64_t *v_full = k_empty + kCaStages;
   uint64_t *v_empty = v_full + kCaStages;
   uint64_t *s_full = v_empty + kCaStages;   // [stream] S is in tensor memory, and the products before it are done
-  uint64_t *p_full = s_full + 2;            // [stream] P' written, O rescaled (128)
-  uint64_t *o_done = p_full + 2;            // [stream] the stream's last product
-  uint64_t *drain = o_done + 2;
-  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+  uint64_t *p_full = s_full + 2;            // [stream][half] 64 positions of P' written, O rescaled (4 warps)
+  uint64_t *o_done = p_full + 4;            // [stream] the stream's last product
+  uint64_t *q_full = o_done + 2;            // q is in shared memory (its rows' threads)
+  uint64_t *drain = q_full + 1;             // [stream] its issuer's last commit
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 2);
   TileMeta *meta = reinterpret_cast<TileMeta *>(sm + S::META);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -292,7 +330,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
   const bool two = k.rows > kCaRows;   // two streams of rows; otherwise both take the same rows, every other tile each
 
   // ---- this thread's row (softmax warps)
-  const int stream = warp >> 2;        // 0, 1: softmax; 2: converters; 3: the MMA issuer
+  const int stream = warp >> 2;        // the warpgroup: 0, 1: softmax streams
   const int lrow = threadIdx.x & 127;
   const int trow = (two && stream == 1 ? kCaRows : 0) + lrow;   // row in the CTA
   const int R = k.row0 + trow;
@@ -317,102 +355,82 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
   }
 
   if (threadIdx.x == 0) {
+    const uint32_t users = two ? 2 : 1;   // streams that use a tile
     for (int s = 0; s < kCaStages; ++s) {
       mbar_init(&k_full[s], 4);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], users);
       mbar_init(&v_full[s], 4);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_empty[s], users);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], kCaRows);
+      mbar_init(&p_full[2 * s], 4);
+      mbar_init(&p_full[2 * s + 1], 4);
       mbar_init(&o_done[s], 1);
+      mbar_init(&drain[s], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(q_full, two ? 2 * kCaRows : kCaRows);
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
 
-  // ---- q as f16 (a power-of-two scale a row brings its largest value to
-  // [1, 2): exact, but for values 2^-24 of the largest and below)
-  float rowfac = 0.0f;
-  if (stream < 2) {
-    uint4 w[D / 8];
-    uint32_t amax = 0;
-    const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(k.first_q + tok) * p.ldq +
-                                                       (int64_t)(kvh * p.G + head) * D);
-    #pragma unroll
-    for (int c = 0; c < D / 8; ++c) w[c] = has_row ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-    #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-      #pragma unroll
-      for (int i = 0; i < 4; ++i) amax = max(amax, max((v[i] << 16) & 0x7FFFFFFFu, v[i] & 0x7FFF0000u));
-    }
-    // 2^e, e the exponent of the largest magnitude, kept where 2^-e is a normal number too
-    const uint32_t ex = min(max(amax >> 23, 1u), 253u);
-    const float up = __uint_as_float((254u - ex) << 23);
-    rowfac = __uint_as_float(ex << 23) * p.scale_log2;
-    if (two || stream == 0) {
-      uint8_t *qs = sm + S::Q + (two ? stream : 0) * S::kOperand;
-      #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-        uint32_t h[4];
-        #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          h[i] = f16_pair(__uint_as_float(v[i] << 16) * up, __uint_as_float(v[i] & 0xFFFF0000u) * up);
-        *reinterpret_cast<uint4 *>(qs + piece_off(lrow, c)) = make_uint4(h[0], h[1], h[2], h[3]);
-      }
-      fence_async_shared();
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  if (stream == 2) {
+  if (stream == 2 || stream == 3) {
     // ------------------------------------------------------------ converters
+    regs_down<kCaRegsConvert>();
     constexpr int LPR = D / 16;           // lanes a row, 16 codes a lane
     constexpr int RP = 32 / LPR;          // rows a load instruction
     constexpr int STEPS = 32 / RP;
-    const int cw = warp - 8;
-    const int piece = lane % LPR;
+    const bool is_k = stream == 2;
+    const int cw = warp & 3;
+    // this lane's row of RP and its 16 codes of the row.  8 neighbouring lanes
+    // hold the same half of an even and an odd row: their 16-byte stores, two
+    // pieces apart in a row, meet 8 different banks under the swizzle.
+    const int row_in = D == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) : lane >> 2;
+    const int piece = D == 128 ? ((lane >> 3) & 1) * 4 + (lane & 3) : lane & 3;
     const int32_t *table = p.block_tables + (int64_t)k.b * p.max_blocks;
     // the slot of this lane's position of local tile j (-1: not read)
     auto slot_of = [&](int j) -> int {
-      if (j >= k.tiles) return -1;
       const int pos = (k.t0 + j) * kCaTile + 32 * cw + lane;
-      if (pos >= k.kv_end) return -1;
+      if (j >= k.tiles || pos >= k.kv_end) return -1;
       const int bi = (int)__umul64hi((uint64_t)pos, p.bs_magic);
       if (bi >= p.max_blocks) return -1;
       const int blk = __ldg(table + bi);
       const int64_t sl = (int64_t)blk * p.block_size + (pos - bi * p.block_size);
       return blk < 0 || sl >= p.num_slots ? -1 : (int)sl;
     };
-    auto load_codes = [&](const uint8_t *cache, int slot, uint4 (&r)[STEPS]) {
+    const uint8_t *codes = (is_k ? p.kc : p.vc) + kvh * D + piece * 16;
+    const int row_bytes = p.Hkv * D;
+    // A position that is not in the cache reads slot 0 instead (a load with no
+    // condition: a select behind it would wait for it).  Its key is masked by
+    // the softmax whatever it holds, its value is zeroed, its scales are
+    // dropped where they are used.
+    auto load_codes = [&](int slot, uint4 (&r)[STEPS]) {
       #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
-        const int s = __shfl_sync(0xffffffffu, slot, i * RP + lane / LPR);
-        r[i] = s >= 0 ? __ldg(reinterpret_cast<const uint4 *>(cache + ((int64_t)s * p.Hkv + kvh) * D) + piece)
-                      : make_uint4(0u, 0u, 0u, 0u);
+        const int s = __shfl_sync(0xffffffffu, slot, i * RP + row_in);
+        r[i] = ld_codes(codes + (int64_t)max(s, 0) * row_bytes);
       }
     };
     auto load_scale = [&](const float *scales, int slot) {
-      return slot >= 0 ? __ldg(scales + (int64_t)slot * p.Hkv + kvh) : 0.0f;
+      return ld_scale(scales + (int64_t)max(slot, 0) * p.Hkv + kvh);
     };
     // bits of a positive finite scale, 0 otherwise
     auto usable = [](float s) -> uint32_t { return s > 0.0f && s < INFINITY ? __float_as_uint(s) : 0u; };
-    // A zero vector has scale 1 whatever its neighbours': taken as 0, or its
-    // 32 positions' weights would crowd out the others'.  Only a scale of
-    // exactly 1 makes the warp look (a wait for memory, but a rare one).
-    auto drop_zero = [&](float scale, int slot) -> float {
+    // The value scale that counts: 0 where there is none.  A zero vector has
+    // scale 1 whatever its neighbours': taken as 0 too, or its 32 positions'
+    // weights would crowd out the others'.  Only a scale of exactly 1 makes
+    // the warp look (a wait for memory, but a rare one).
+    auto value_scale = [&](float scale, int slot) -> float {
       const bool one = slot >= 0 && scale == 1.0f;
-      if (!__any_sync(0xffffffffu, one)) return scale;
+      if (!__any_sync(0xffffffffu, one)) return slot >= 0 ? scale : 0.0f;
       uint32_t any = 0;
       if (one) {
         const uint4 *row = reinterpret_cast<const uint4 *>(p.vc + ((int64_t)slot * p.Hkv + kvh) * D);
@@ -422,221 +440,248 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
           any |= v.x | v.y | v.z | v.w;
         }
       }
-      return one && (any & 0x7F7F7F7Fu) == 0 ? 0.0f : scale;
+      return slot < 0 || (one && (any & 0x7F7F7F7Fu) == 0) ? 0.0f : scale;
     };
-    // 16 codes of row r as f16: two 16-byte pieces.  Lanes of the second half
-    // of a row store their odd piece first, so that the 8 lanes of a row meet
-    // 8 different banks.
-    auto store = [&](uint8_t *dst, int r, const uint32_t (&h)[8]) {
-      const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-      const bool odd = D == 128 && piece >= 4;
-      *reinterpret_cast<uint4 *>(dst + piece_off(r, 2 * piece + (odd ? 1 : 0))) = odd ? b : a;
-      *reinterpret_cast<uint4 *>(dst + piece_off(r, 2 * piece + (odd ? 0 : 1))) = odd ? a : b;
-    };
-    // the value scales' reference: 2^-6 of a power of two >= the largest
-    // usable one, in [2^-90, 2^120] (1: none)
-    auto value_ref = [](uint32_t top) -> uint32_t {
-      const uint32_t up = (top + 0x007FFFFFu) & 0x7F800000u;
-      return top != 0 ? min(max(up, 43u << 23) - (6u << 23), 247u << 23) : 127u << 23;
-    };
-    // K' of tile j, and what the softmax needs of the tile's scales
-    auto put_k = [&](int j, const uint4 (&r)[STEPS], float scale, float v_scale, int slot) -> bool {
-      const int s = j % kCaStages;
+    // The reference of 32 scales: a power of two >= the largest usable one,
+    // less `below` powers, in [2^-90, 2^120] (1: there is none); as bits.
+    auto reference = [&](float scale, uint32_t below) -> uint32_t {
       const uint32_t top = __reduce_max_sync(0xffffffffu, usable(scale));
-      const float kref = top != 0 ? __uint_as_float(top) : 1.0f;
-      const float ratio = __fdiv_rn(scale, kref);
-      const float hi = __half2float(__float2half_rn(ratio));
-      const uint32_t split2 = f16_pair(hi, ratio - hi);   // infinite scales: NaN, in their column alone
-      const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
-      const uint32_t vb = value_ref(__reduce_max_sync(0xffffffffu, usable(v_scale)));
-      const bool w = j < kCaStages || mbar_wait(&k_empty[s], (uint32_t)(j / kCaStages - 1) & 1u);
-      if (!__all_sync(0xffffffffu, w)) return false;
-      if (lane == 0) {
-        TileMeta &t = meta[j % kCaMeta];
-        t.kref[cw] = kref;
-        t.valid[cw] = valid;
-        t.lv[cw] = (float)((int)(vb >> 23) - 127);
-        t.inv_vref[cw] = __uint_as_float((254u << 23) - vb);
-      }
-      uint8_t *dst = sm + S::K + s * S::kOperand;
-      #pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const int row = i * RP + lane / LPR;
-        const uint32_t f = __shfl_sync(0xffffffffu, split2, row);
-        const uint32_t hi2 = __byte_perm(f, f, 0x1010), lo2 = __byte_perm(f, f, 0x3232);
-        const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-        uint32_t h[8];
-        #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t c = e4m3_f16x2(w[e >> 1] >> (16 * (e & 1)));
-          h[e] = fma_f16x2(c, hi2, mul_f16x2(c, lo2));
-        }
-        store(dst, 32 * cw + row, h);
-      }
+      const uint32_t up = (top + 0x007FFFFFu) & 0x7F800000u;
+      return top != 0 ? min(max(up, 43u << 23) - (below << 23), 247u << 23) : 127u << 23;
+    };
+    // 2^-x of a power of two 2^x
+    auto inverse = [](uint32_t bits) { return __uint_as_float((254u << 23) - bits); };
+    // 16 codes of row r as f16
+    auto store = [&](uint8_t *dst, int r, const uint32_t (&h)[8]) {
+      *reinterpret_cast<uint4 *>(dst + piece_off(r, 2 * piece)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4 *>(dst + piece_off(r, 2 * piece + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+    };
+    // stage j % kCaStages is free (its products of kCaStages tiles ago are done)
+    auto wait_free = [&](uint64_t *empty, int j) -> bool {
+      const bool w = j < kCaStages || mbar_wait(&empty[j % kCaStages], (uint32_t)(j / kCaStages - 1) & 1u);
+      return __all_sync(0xffffffffu, w);
+    };
+    auto publish = [&](uint64_t *full, int j) {
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full[s]);
-      return true;
+      if (lane == 0) mbar_arrive(&full[j % kCaStages]);
     };
-    auto put_v = [&](int j, uint4 (&r)[STEPS], float scale) -> bool {
-      const int s = j % kCaStages;
-      const float inv = __uint_as_float((254u << 23) - value_ref(__reduce_max_sync(0xffffffffu, usable(scale))));
-      const uint32_t ratio = f16_pair(scale * inv, scale * inv);
-      // tiles that some rows see in part: P' = 0 must cancel a value that is
-      // not finite, so its vector is zeroed and marked for the rows that see it
-      const bool partial = (k.t0 + j + 1) * kCaTile > all_see;
-      uint32_t nan = 0;
-      if (partial) {
-        nan = __ballot_sync(0xffffffffu, !(scale < INFINITY));
+
+    uint4 r[STEPS];
+    int slot = slot_of(0), next = slot_of(1);
+    float vsc = load_scale(p.vs, slot);
+    bool ok = true;
+    if (is_k) {
+      float ksc = load_scale(p.ks, slot);
+      load_codes(slot, r);
+      #pragma unroll 1
+      for (int j = 0; j < k.tiles; ++j) {
+        const int after = slot_of(j + 2);
+        // K' = code * ks / kref, and what the softmax needs of the tile's scales
+        const float scale = slot >= 0 ? ksc : 0.0f;
+        const uint32_t kb = reference(scale, 0), vb = reference(value_scale(vsc, slot), 6);
+        const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
+        const float ratio = scale * inverse(kb);
+        const float hi = __half2float(__float2half_rn(ratio));
+        const uint32_t split2 = f16_pair(hi, ratio - hi);   // infinite scales: NaN, in their column alone
+        ok = wait_free(k_empty, j);
+        if (!ok) break;
+        if (lane == 0) {
+          TileMeta &t = meta[j % kCaMeta];
+          t.kref[cw] = __uint_as_float(kb);
+          t.valid[cw] = valid;
+          t.lv[cw] = (float)((int)(vb >> 23) - 127);
+          t.inv_vref[cw] = inverse(vb);
+        }
+        uint8_t *dst = sm + S::K + (j % kCaStages) * S::kOperand;
         #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
+          const int row = i * RP + row_in;
+          const uint32_t f = __shfl_sync(0xffffffffu, split2, row);
+          const uint32_t hi2 = __byte_perm(f, f, 0x1010), lo2 = __byte_perm(f, f, 0x3232);
           const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-          bool bad = (nan >> (i * RP + lane / LPR)) & 1u;
+          uint32_t h[8];
           #pragma unroll
-          for (int e = 0; e < 4; ++e) bad = bad || (((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-          const uint32_t lanes = __ballot_sync(0xffffffffu, bad);
-          if (bad) r[i] = make_uint4(0u, 0u, 0u, 0u);
-          #pragma unroll
-          for (int g = 0; g < RP; ++g)
-            if ((lanes >> (g * LPR)) & ((1u << LPR) - 1u)) nan |= 1u << (i * RP + g);
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t c = e4m3_f16x2(w[e >> 1] >> (16 * (e & 1)));
+            h[e] = fma_f16x2(c, hi2, mul_f16x2(c, lo2));
+          }
+          store(dst, 32 * cw + row, h);
         }
+        slot = next;
+        next = after;
+        ksc = load_scale(p.ks, slot);
+        vsc = load_scale(p.vs, slot);
+        load_codes(slot, r);
+        publish(k_full, j);
       }
-      const bool w = j < kCaStages || mbar_wait(&v_empty[s], (uint32_t)(j / kCaStages - 1) & 1u);
-      if (!__all_sync(0xffffffffu, w)) return false;
-      if (partial && lane == 0) meta[j % kCaMeta].nan[cw] = nan;
-      uint8_t *dst = sm + S::V + s * S::kOperand;
-      #pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const int row = i * RP + lane / LPR;
-        uint32_t f = __shfl_sync(0xffffffffu, ratio, row);
-        if (partial && ((nan >> row) & 1u)) f = 0u;
-        const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-        uint32_t h[8];
-        #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = mul_f16x2(e4m3_f16x2(w[e >> 1] >> (16 * (e & 1))), f);
-        store(dst, 32 * cw + row, h);
-      }
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&v_full[s]);
-      return true;
-    };
-    uint4 kr[STEPS], vr[STEPS];
-    int s0 = slot_of(0), s1 = slot_of(1), s2 = slot_of(2);
-    load_codes(p.kc, s0, kr);
-    float ksc = load_scale(p.ks, s0), vsc = load_scale(p.vs, s0), vsc1 = load_scale(p.vs, s1);
-    load_codes(p.vc, s0, vr);
-    vsc = drop_zero(vsc, s0);
-    bool ok = put_k(0, kr, ksc, vsc, s0);
-    ksc = load_scale(p.ks, s1);
-    load_codes(p.kc, s1, kr);
-    #pragma unroll 1
-    for (int j = 0; j < k.tiles && ok; ++j) {
-      // here: s0, s1, s2 the slots of tiles j, j + 1, j + 2; kr, ksc of j + 1; vr, vsc of j; vsc1 of j + 1
-      const int s3 = slot_of(j + 3);
-      if (j + 1 < k.tiles) {
-        vsc1 = drop_zero(vsc1, s1);
-        ok = put_k(j + 1, kr, ksc, vsc1, s1);
+    } else {
+      load_codes(slot, r);
+      #pragma unroll 1
+      for (int j = 0; j < k.tiles; ++j) {
+        const int after = slot_of(j + 2);
+        // V' = code * vs / vref
+        const float scale = value_scale(vsc, slot);
+        const float inv = inverse(reference(scale, 6));
+        const uint32_t ratio = f16_pair(scale * inv, scale * inv);
+        const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
+        if (valid != 0xffffffffu) {
+          #pragma unroll
+          for (int i = 0; i < STEPS; ++i)
+            if (!((valid >> (i * RP + row_in)) & 1u)) r[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        // tiles that some rows see in part: P' = 0 must cancel a value that is
+        // not finite, so its vector is zeroed and marked for the rows that see it
+        uint32_t nan = 0;
+        const bool partial = (k.t0 + j + 1) * kCaTile > all_see;
+        if (partial) {
+          nan = __ballot_sync(0xffffffffu, !(scale < INFINITY));
+          #pragma unroll
+          for (int i = 0; i < STEPS; ++i) {
+            const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+            bool bad = false;
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) bad = bad || (((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+            if (bad) r[i] = make_uint4(0u, 0u, 0u, 0u);
+            nan |= __reduce_or_sync(0xffffffffu, bad ? 1u << (i * RP + row_in) : 0u);
+          }
+        }
+        ok = wait_free(v_empty, j);
         if (!ok) break;
-        ksc = load_scale(p.ks, s2);
-        load_codes(p.kc, s2, kr);
+        if (partial && lane == 0) meta[j % kCaMeta].nan[cw] = nan;
+        uint8_t *dst = sm + S::V + (j % kCaStages) * S::kOperand;
+        #pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const int row = i * RP + row_in;
+          uint32_t f = __shfl_sync(0xffffffffu, ratio, row);
+          if ((nan >> row) & 1u) f = 0u;
+          const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+          uint32_t h[8];
+          #pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] = mul_f16x2(e4m3_f16x2(w[e >> 1] >> (16 * (e & 1))), f);
+          store(dst, 32 * cw + row, h);
+        }
+        slot = next;
+        next = after;
+        vsc = load_scale(p.vs, slot);
+        load_codes(slot, r);
+        publish(v_full, j);
       }
-      ok = put_v(j, vr, vsc);
-      if (!ok) break;
-      vsc = vsc1;
-      vsc1 = load_scale(p.vs, s2);
-      load_codes(p.vc, s1, vr);
-      s1 = s2;
-      s2 = s3;
     }
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutChunk);
-  } else if (stream == 3) {
-    // ------------------------------------------------------------ MMA issuer
-    if (elect_one()) {
+  } else if (stream == 4) {
+    // ------------------------------------------------------------ MMA issuers
+    // A warp a stream, so that a stream's products wait for its own softmax alone.
+    regs_down<kCaRegsIssuer>();
+    if (warp < 18 && elect_one()) {
       constexpr uint32_t idesc_qk = idesc_f16(kCaTile, false);
       constexpr uint32_t idesc_pv = idesc_f16(D, true);
-      bool ok = true;
+      const int s = warp - 16;
+      const int count = two ? (s == 0 ? k.tiles0 : k.tiles) : (k.tiles + 1 - s) >> 1;
       auto wait_full = [&](uint64_t *bar, int j) {
         return mbar_wait(&bar[j % kCaStages], (uint32_t)(j / kCaStages) & 1u);
       };
-      // S of stream s for tile j: behind the stream's product before it, whose
-      // P' it overwrites (products of one thread run in order)
-      auto qk = [&](int s, int j) {
-        const uint32_t qb = smem_u32(sm + S::Q + (two ? s : 0) * S::kOperand);
-        const uint32_t kb = smem_u32(sm + S::K + (j % kCaStages) * S::kOperand);
+      const uint32_t q_desc = desc_k_major(smem_u32(sm + S::Q)) + (two ? s : 0) * (S::kOperand >> 4);
+      const uint32_t k_desc = desc_k_major(smem_u32(sm + S::K)), v_desc = desc_mn_major(smem_u32(sm + S::V));
+      const uint32_t ts = tmem_base + s * 128, to = tmem_base + 256 + s * D;
+      // S of tile j: behind the product before it, whose P' it overwrites
+      // (products of one thread run in order)
+      auto qk = [&](int j) {
+        const uint32_t b = k_desc + (j % kCaStages) * (S::kOperand >> 4);
+        mma_f16_ss<false>(ts, q_desc, b, idesc_qk);
         #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * (kCaRows * 128) + (kk & 3) * 32;
-          mma_f16_ss(tmem_base + s * 128, sw128_kmajor_desc(qb + off), sw128_kmajor_desc(kb + off), idesc_qk,
-                     kk > 0 ? 1u : 0u);
+        for (int kk = 1; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * (kCaRows * 128) + (kk & 3) * 32) >> 4;
+          mma_f16_ss<true>(ts, q_desc + off, b + off, idesc_qk);
         }
         mma_commit(&s_full[s]);
+        mma_commit(&k_empty[j % kCaStages]);
       };
-      auto pv = [&](int s, int j, bool first) {
-        const uint32_t vb = smem_u32(sm + S::V + (j % kCaStages) * S::kOperand);
+      // half of O += P' V' of tile j
+      auto pv = [&](int j, int half, bool first) {
+        const uint32_t b = v_desc + (j % kCaStages) * (S::kOperand >> 4);
         #pragma unroll
-        for (int kk = 0; kk < kCaTile / 16; ++kk)
-          mma_f16_ts(tmem_base + 256 + s * D, tmem_base + s * 128 + kk * 8,
-                     sw128_mn_desc(vb + kk * 16 * 128, kCaRows * 128), idesc_pv, !first || kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < kCaTile / 32; ++kk)
+          mma_f16_ts(to, ts + half * 32 + kk * 8, b + (half * 64 + kk * 16) * (128 >> 4), idesc_pv,
+                     kk > 0 || !first ? 1u : 0u);
       };
-      if (two) {
-        ok = wait_full(k_full, 0);
-        if (ok) {
-          tc_fence_after();
-          if (k.tiles0 > 0) qk(0, 0);
-          qk(1, 0);
-          mma_commit(&k_empty[0]);
-        }
-        for (int j = 0; j < k.tiles && ok; ++j) {
-          for (int s = j < k.tiles0 ? 0 : 1; s < 2 && ok; ++s) {
-            ok = wait_full(v_full, j) && mbar_wait(&p_full[s], (uint32_t)j & 1u);
-            if (!ok) break;
-            tc_fence_after();
-            pv(s, j, j == 0);
-            const int mine = s == 0 ? k.tiles0 : k.tiles;
-            if (j + 1 == mine) mma_commit(&o_done[s]);
-            if (s == 1) mma_commit(&v_empty[j % kCaStages]);
-            if (j + 1 < mine) {
-              ok = wait_full(k_full, j + 1);
-              if (!ok) break;
-              tc_fence_after();
-              qk(s, j + 1);
-              if (s == 1) mma_commit(&k_empty[(j + 1) % kCaStages]);
-            }
-          }
-        }
-      } else {
-        for (int j = 0; j < min(2, k.tiles) && ok; ++j) {
-          ok = wait_full(k_full, j);
+      auto tile = [&](int it) { return two ? it : 2 * it + s; };
+      bool ok = mbar_wait(q_full, 0);
+      if (ok && count > 0) {
+        ok = wait_full(k_full, tile(0));
+        tc_fence_after();
+        if (ok) qk(tile(0));
+      }
+      for (int it = 0; it < count && ok; ++it) {
+        const int j = tile(it);
+        ok = wait_full(v_full, j) && mbar_wait(&p_full[2 * s], (uint32_t)it & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        pv(j, 0, it == 0);
+        ok = mbar_wait(&p_full[2 * s + 1], (uint32_t)it & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        pv(j, 1, false);
+        mma_commit(&v_empty[j % kCaStages]);
+        if (it + 1 == count) {
+          mma_commit(&o_done[s]);
+        } else {
+          ok = wait_full(k_full, tile(it + 1));
           if (!ok) break;
           tc_fence_after();
-          qk(j, j);
-          mma_commit(&k_empty[j % kCaStages]);
+          qk(tile(it + 1));
         }
-        for (int j = 0; j < k.tiles && ok; ++j) {
-          const int s = j & 1;
-          ok = wait_full(v_full, j) && mbar_wait(&p_full[s], (uint32_t)(j >> 1) & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          pv(s, j, j < 2);
-          mma_commit(&v_empty[j % kCaStages]);
-          if (j + 2 >= k.tiles) mma_commit(&o_done[s]);
-          if (j + 2 < k.tiles) {
-            ok = wait_full(k_full, j + 2);
-            if (!ok) break;
-            tc_fence_after();
-            qk(s, j + 2);
-            mma_commit(&k_empty[(j + 2) % kCaStages]);
-          }
-        }
+      }
+      // tiles that only the other stream needs: this one's share of freeing them
+      for (int j = count; two && j < k.tiles && ok; ++j) {
+        ok = wait_full(k_full, j);
+        if (ok) mbar_arrive(&k_empty[j % kCaStages]);
+        ok = ok && wait_full(v_full, j);
+        if (ok) mbar_arrive(&v_empty[j % kCaStages]);
       }
       if (!ok) atomicOr(p.status, kStatusTimeoutChunk);
       // every product issued has completed before the CTA ends
-      mma_commit(drain);
-      mbar_wait(drain, 0);
+      mma_commit(&drain[s]);
+      mbar_wait(&drain[s], 0);
     }
   } else {
     // ------------------------------------------------------------ softmax
+    regs_up<kCaRegsSoftmax>();
+    // q as f16 (a power-of-two scale a row brings its largest value to [1, 2):
+    // exact, but for values 2^-24 of the largest and below)
+    float rowfac;
+    {
+      uint4 w[D / 8];
+      uint32_t amax = 0;
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(k.first_q + tok) * p.ldq +
+                                                         (int64_t)(kvh * p.G + head) * D);
+      #pragma unroll
+      for (int c = 0; c < D / 8; ++c) w[c] = has_row ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      #pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) amax = max(amax, max((v[i] << 16) & 0x7FFFFFFFu, v[i] & 0x7FFF0000u));
+      }
+      // 2^e, e the exponent of the largest magnitude, kept where 2^-e is a normal number too
+      const uint32_t ex = min(max(amax >> 23, 1u), 253u);
+      const float up = __uint_as_float((254u - ex) << 23);
+      rowfac = __uint_as_float(ex << 23) * p.scale_log2;
+      if (two || stream == 0) {
+        uint8_t *qs = sm + S::Q + (two ? stream : 0) * S::kOperand;
+        #pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+          uint32_t h[4];
+          #pragma unroll
+          for (int i = 0; i < 4; ++i)
+            h[i] = f16_pair(__uint_as_float(v[i] << 16) * up, __uint_as_float(v[i] & 0xFFFF0000u) * up);
+          *reinterpret_cast<uint4 *>(qs + piece_off(lrow, c)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        fence_async_shared();
+        mbar_arrive(q_full);
+      }
+    }
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem_base + lane_addr + stream * 128;        // S, then P'
     const uint32_t to = tmem_base + lane_addr + 256 + stream * D;    // O
@@ -652,97 +697,113 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       ok = __all_sync(0xffffffffu, arrived);
       if (!ok) break;
       tc_fence_after();
+      // the first half's scores are under way while the tile's scales and
+      // masks are fetched, the second half's while the first's maximum is taken
+      uint32_t x[4][32];
+      tmem_ld_32x32b_x32(ts, x[0]);
+      tmem_ld_32x32b_x32(ts + 32, x[1]);
       const TileMeta &tm = meta[j % kCaMeta];
       uint32_t mask[4];
       bool full = true;
+      // t = S * cf: cf at least the smallest normal number, so that a masked -inf stays one
+      float cf[4], lv[4];
       #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int n = sees - ((k.t0 + j) * kCaTile + 32 * c);
         const uint32_t causal = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
         mask[c] = tm.valid[c] & causal;
         full = full && mask[c] == 0xffffffffu;
+        cf[c] = fmaxf(tm.kref[c] * rowfac, 0x1p-126f);
+        lv[c] = tm.lv[c];
       }
       full = __all_sync(0xffffffffu, full);
-      float cf[4];
-      #pragma unroll
-      for (int c = 0; c < 4; ++c) cf[c] = tm.kref[c] * rowfac;
-      // the tile's largest t + log2 vref
-      float top = -INFINITY;
-      #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32];
-        tmem_ld_32x32b_x32(ts + 32 * c, x);
-        tmem_wait_ld();
-        float m0 = -INFINITY, m1 = -INFINITY;
-        if (full) {
+      tmem_wait_ld();
+      arrived32(x[0]);
+      arrived32(x[1]);
+      tmem_ld_32x32b_x32(ts + 64, x[2]);
+      tmem_ld_32x32b_x32(ts + 96, x[3]);
+      auto hide = [&](int c) {
+        #pragma unroll
+        for (int i = 0; i < 32; ++i) x[c][i] = (mask[c] >> i) & 1u ? x[c][i] : 0xFF800000u;
+      };
+      auto largest = [&](int c) {
+        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        #pragma unroll
+        for (int i = 0; i < 32; i += 8) {
           #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            m0 = fmaxf(fmaxf(m0, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-            m1 = fmaxf(fmaxf(m1, __uint_as_float(x[i + 2])), __uint_as_float(x[i + 3]));
-          }
-          top = fmaxf(top, fmaf(fmaxf(m0, m1), cf[c], tm.lv[c]));
-        } else {
-          #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            m0 = fmaxf(m0, (mask[c] >> i) & 1u ? __uint_as_float(x[i]) * cf[c] : -INFINITY);
-          top = fmaxf(top, m0 + tm.lv[c]);
+          for (int e = 0; e < 4; ++e)
+            m[e] = fmaxf(fmaxf(m[e], __uint_as_float(x[c][i + 2 * e])), __uint_as_float(x[c][i + 2 * e + 1]));
         }
+        return fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), cf[c], lv[c]);
+      };
+      if (!full) {
+        hide(0);
+        hide(1);
       }
+      // the tile's largest t + log2 vref
+      float top = fmaxf(largest(0), largest(1));
+      tmem_wait_ld();
+      arrived32(x[2]);
+      arrived32(x[3]);
+      if (!full) {
+        hide(2);
+        hide(3);
+      }
+      top = fmaxf(top, fmaxf(largest(2), largest(3)));
       const bool need = top > r + kCaLazy;
       if (__any_sync(0xffffffffu, need)) {
         const float f = need && r != -INFINITY ? ex2(r - top) : 1.0f;
         if (need) r = top;
         l *= f;
         if (it > 0) {
-          #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t x[32];
-            tmem_ld_32x32b_x32(to + 32 * c, x);
+          #pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(to + 16 * c, o);
             tmem_wait_ld();
             #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-            tmem_st_32x32b_x32(to + 32 * c, x);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st_32x32b_x16(to + 16 * c, o);
           }
         }
       }
       const float rs = r == -INFINITY ? 0.0f : r;
       #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t x[32], y[16];
-        tmem_ld_32x32b_x32(ts + 32 * c, x);
-        tmem_wait_ld();
-        const float bias = tm.lv[c] - rs;
+        uint32_t y[16];
+        const float bias = lv[c] - rs;
         const uint64_t cf2 = pack_f32x2(cf[c], cf[c]), b2 = pack_f32x2(bias, bias);
         uint64_t sum0 = 0, sum1 = 0;
         #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float2 t = unpack_f32x2(
-              fma_f32x2(pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cf2, b2));
-          float a = ex2(t.x), b = ex2(t.y);
-          if (!full) {
-            a = (mask[c] >> (2 * i)) & 1u ? a : 0.0f;
-            b = (mask[c] >> (2 * i + 1)) & 1u ? b : 0.0f;
-          }
+              fma_f32x2(pack_f32x2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), cf2, b2));
+          const float a = ex2(t.x), b = ex2(t.y);
           y[i] = f16_pair(a, b);
           if (i & 1) sum1 = add_f32x2(sum1, pack_f32x2(a, b));
           else sum0 = add_f32x2(sum0, pack_f32x2(a, b));
         }
-        const float2 sm2 = unpack_f32x2(add_f32x2(sum0, sum1));
-        l = fmaf(sm2.x + sm2.y, tm.inv_vref[c], l);
+        const float2 both = unpack_f32x2(add_f32x2(sum0, sum1));
+        l = fmaf(both.x + both.y, tm.inv_vref[c], l);
         tmem_st_32x32b_x16(ts + 16 * c, y);
+        if (c & 1) {   // half of P' is there: its products can start
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * stream + (c >> 1)]);
+        }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&p_full[stream]);
     }
     if (ok && count > 0) ok = mbar_wait(&o_done[stream], 0);
+    // stream 1 hands its O over in the K ring: the other stream's products have to be done too
+    if (ok && !two && stream == 1 && count > 0) ok = mbar_wait(&o_done[0], 0);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutChunk);
     tc_fence_after();
     if (!ok) l = 0.0f;
     float f0 = l == 0.0f ? 0.0f : 1.0f;   // factor of this stream's O
     float f1 = 0.0f;                      // factor of the other stream's, when the two are joined
-    float *joined = reinterpret_cast<float *>(sm + S::K);   // [D][128], in the K ring: every S is done
+    float *joined = reinterpret_cast<float *>(sm + S::K);   // [D][128], in the K ring
     float2 *ml1 = reinterpret_cast<float2 *>(sm + S::ML);
     if (!two) {
       if (stream == 1) {
@@ -823,7 +884,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }
