@@ -27,7 +27,9 @@
 // 1 however the value scales spread, and the sum of 2^(t - r) is that of P' /
 // vref.  r moves (and O, in tensor memory, is rescaled) only when a tile
 // exceeds it by more than 8, so P' < 2^8.  P' overwrites S in place.
-// While one stream is in the softmax the other's products run.  A CTA with 128
+// A tile goes through in halves of 64 positions, each with scores of its own in
+// tensor memory, so that a stream's products of one half run while its softmax
+// works on the other, and both streams' softmaxes never wait for theirs.  A CTA with 128
 // rows or fewer gives both streams the same rows and every other tile each,
 // and joins them at the end.
 //
@@ -52,9 +54,9 @@ namespace {
 // Warpgroups: 0, 1 the softmax of a stream each, 2 converts K, 3 converts V,
 // 4 issues the products (its first two warps, a stream each).
 constexpr int kCaThreads = 640;
-// Registers a thread once the roles part (the softmax keeps a row's 128
-// scores): 2 x 160 + 2 x 64 + 32 = 5 x 96, what the CTA is launched with.
-constexpr int kCaRegsSoftmax = 160, kCaRegsConvert = 64, kCaRegsIssuer = 32;
+// Registers a thread once the roles part (the softmax keeps 64 of a row's
+// scores): 2 x 136 + 2 x 80 + 48 = 5 x 96, what the CTA is launched with.
+constexpr int kCaRegsSoftmax = 136, kCaRegsConvert = 80, kCaRegsIssuer = 48;
 constexpr int kCaRows = 128;      // rows a stream
 constexpr int kCaTile = 128;      // positions a tile
 constexpr int kCaStages = 2;      // stages of the K ring and of the V ring
@@ -99,7 +101,7 @@ struct CaSmem {
   static constexpr int META = V + kCaStages * kOperand;
   static constexpr int ML = META + kCaMeta * (int)sizeof(TileMeta);  // [row]: r and l of stream 1 when joined
   static constexpr int BARS = ML + kCaRows * 8;
-  static constexpr int kBars = 4 * kCaStages + 4 * 2 + 3;
+  static constexpr int kBars = 4 * kCaStages + 3 * 4 + 3;
   static constexpr int BYTES = 1024 + BARS + kBars * 8 + 16;
 };
 
@@ -140,11 +142,11 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two E4M3 codes (low byte first) as f16, exact.
-__device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two));
-  return r;
+// Four E4M3 codes (lowest byte first) as two pairs of f16, exact.
+__device__ __forceinline__ void e4m3_f16x4(uint32_t four, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -213,6 +215,12 @@ __device__ __forceinline__ float ld_scale(const float *ptr) {
   float v;
   asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(ptr));
   return v;
+}
+
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return r;
 }
 
 // Ties loaded registers to the wait before: nothing that reads them moves above it.
@@ -302,10 +310,10 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
   uint64_t *k_empty = k_full + kCaStages;   // [stage] its products are done
   uint64_t *v_full = k_empty + kCaStages;
   uint64_t *v_empty = v_full + kCaStages;
-  uint64_t *s_full = v_empty + kCaStages;   // [stream] S is in tensor memory, and the products before it are done
-  uint64_t *p_full = s_full + 2;            // [stream][half] 64 positions of P' written, O rescaled (4 warps)
-  uint64_t *o_done = p_full + 4;            // [stream] the stream's last product
-  uint64_t *q_full = o_done + 2;            // q is in shared memory (its rows' threads)
+  uint64_t *s_full = v_empty + kCaStages;   // [stream][half] S of 64 positions is in tensor memory
+  uint64_t *p_full = s_full + 4;            // [stream][half] their P' is written, O rescaled (4 warps)
+  uint64_t *o_done = p_full + 4;            // [stream][half] their product is done
+  uint64_t *q_full = o_done + 4;            // q is in shared memory (its rows' threads)
   uint64_t *drain = q_full + 1;             // [stream] its issuer's last commit
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 2);
   TileMeta *meta = reinterpret_cast<TileMeta *>(sm + S::META);
@@ -362,13 +370,13 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       mbar_init(&v_full[s], 4);
       mbar_init(&v_empty[s], users);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[2 * s], 4);
-      mbar_init(&p_full[2 * s + 1], 4);
+      mbar_init(&p_full[s], 4);
       mbar_init(&o_done[s], 1);
-      mbar_init(&drain[s], 1);
     }
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     mbar_init(q_full, two ? 2 * kCaRows : kCaRows);
     fence_barrier_init();
   }
@@ -502,9 +510,11 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
           const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
           uint32_t h[8];
           #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t c = e4m3_f16x2(w[e >> 1] >> (16 * (e & 1)));
-            h[e] = fma_f16x2(c, hi2, mul_f16x2(c, lo2));
+          for (int e = 0; e < 8; e += 2) {
+            uint32_t a, b;
+            e4m3_f16x4(w[e >> 1], a, b);
+            h[e] = fma_f16x2(a, hi2, mul_f16x2(a, lo2));
+            h[e + 1] = fma_f16x2(b, hi2, mul_f16x2(b, lo2));
           }
           store(dst, 32 * cw + row, h);
         }
@@ -558,7 +568,12 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
           const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
           uint32_t h[8];
           #pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = mul_f16x2(e4m3_f16x2(w[e >> 1] >> (16 * (e & 1))), f);
+          for (int e = 0; e < 8; e += 2) {
+            uint32_t a, b;
+            e4m3_f16x4(w[e >> 1], a, b);
+            h[e] = mul_f16x2(a, f);
+            h[e + 1] = mul_f16x2(b, f);
+          }
           store(dst, 32 * cw + row, h);
         }
         slot = next;
@@ -574,7 +589,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     // A warp a stream, so that a stream's products wait for its own softmax alone.
     regs_down<kCaRegsIssuer>();
     if (warp < 18 && elect_one()) {
-      constexpr uint32_t idesc_qk = idesc_f16(kCaTile, false);
+      constexpr uint32_t idesc_qk = idesc_f16(kCaTile / 2, false);
       constexpr uint32_t idesc_pv = idesc_f16(D, true);
       const int s = warp - 16;
       const int count = two ? (s == 0 ? k.tiles0 : k.tiles) : (k.tiles + 1 - s) >> 1;
@@ -584,52 +599,53 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       const uint32_t q_desc = desc_k_major(smem_u32(sm + S::Q)) + (two ? s : 0) * (S::kOperand >> 4);
       const uint32_t k_desc = desc_k_major(smem_u32(sm + S::K)), v_desc = desc_mn_major(smem_u32(sm + S::V));
       const uint32_t ts = tmem_base + s * 128, to = tmem_base + 256 + s * D;
-      // S of tile j: behind the product before it, whose P' it overwrites
-      // (products of one thread run in order)
-      auto qk = [&](int j) {
-        const uint32_t b = k_desc + (j % kCaStages) * (S::kOperand >> 4);
-        mma_f16_ss<false>(ts, q_desc, b, idesc_qk);
+      // S of half h of tile j: behind the half's product before it, whose P'
+      // it overwrites (products of one thread run in order)
+      auto qk = [&](int j, int h) {
+        const uint32_t b = k_desc + (j % kCaStages) * (S::kOperand >> 4) + h * (64 * 128 >> 4);
+        mma_f16_ss<false>(ts + h * 64, q_desc, b, idesc_qk);
         #pragma unroll
         for (int kk = 1; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * (kCaRows * 128) + (kk & 3) * 32) >> 4;
-          mma_f16_ss<true>(ts, q_desc + off, b + off, idesc_qk);
+          mma_f16_ss<true>(ts + h * 64, q_desc + off, b + off, idesc_qk);
         }
-        mma_commit(&s_full[s]);
-        mma_commit(&k_empty[j % kCaStages]);
+        mma_commit(&s_full[2 * s + h]);
+        if (h == 1) mma_commit(&k_empty[j % kCaStages]);
       };
-      // half of O += P' V' of tile j
-      auto pv = [&](int j, int half, bool first) {
-        const uint32_t b = v_desc + (j % kCaStages) * (S::kOperand >> 4);
+      // O += P' V' of half h of tile j
+      auto pv = [&](int j, int h, bool first) {
+        const uint32_t b = v_desc + (j % kCaStages) * (S::kOperand >> 4) + h * (64 * 128 >> 4);
         #pragma unroll
-        for (int kk = 0; kk < kCaTile / 32; ++kk)
-          mma_f16_ts(to, ts + half * 32 + kk * 8, b + (half * 64 + kk * 16) * (128 >> 4), idesc_pv,
-                     kk > 0 || !first ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16_ts(to, ts + h * 64 + kk * 8, b + kk * (16 * 128 >> 4), idesc_pv, kk > 0 || !first ? 1u : 0u);
+        mma_commit(&o_done[2 * s + h]);
+        if (h == 1) mma_commit(&v_empty[j % kCaStages]);
       };
       auto tile = [&](int it) { return two ? it : 2 * it + s; };
       bool ok = mbar_wait(q_full, 0);
       if (ok && count > 0) {
         ok = wait_full(k_full, tile(0));
         tc_fence_after();
-        if (ok) qk(tile(0));
+        if (ok) {
+          qk(tile(0), 0);
+          qk(tile(0), 1);
+        }
       }
       for (int it = 0; it < count && ok; ++it) {
-        const int j = tile(it);
-        ok = wait_full(v_full, j) && mbar_wait(&p_full[2 * s], (uint32_t)it & 1u);
-        if (!ok) break;
-        tc_fence_after();
-        pv(j, 0, it == 0);
-        ok = mbar_wait(&p_full[2 * s + 1], (uint32_t)it & 1u);
-        if (!ok) break;
-        tc_fence_after();
-        pv(j, 1, false);
-        mma_commit(&v_empty[j % kCaStages]);
-        if (it + 1 == count) {
-          mma_commit(&o_done[s]);
-        } else {
-          ok = wait_full(k_full, tile(it + 1));
+        const int j = tile(it), next = it + 1 < count ? tile(it + 1) : -1;
+        ok = wait_full(v_full, j);
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ok = ok && mbar_wait(&p_full[2 * s + h], (uint32_t)it & 1u);
           if (!ok) break;
           tc_fence_after();
-          qk(tile(it + 1));
+          pv(j, h, it + h == 0);
+          if (next >= 0) {
+            ok = h == 1 || wait_full(k_full, next);
+            if (!ok) break;
+            tc_fence_after();
+            qk(next, h);
+          }
         }
       }
       // tiles that only the other stream needs: this one's share of freeing them
@@ -690,72 +706,67 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     const int sees = has_row ? k.m - k.n + tok + 1 : 0x7FFFFFFF;
     float r = -INFINITY, l = 0.0f;
     bool ok = true;
+    // half a tile, 64 positions, a turn
     #pragma unroll 1
-    for (int it = 0; it < count; ++it) {
+    for (int u = 0; u < 2 * count; ++u) {
+      const int it = u >> 1, h = u & 1;
       const int j = two ? it : 2 * it + stream;
-      const bool arrived = mbar_wait(&s_full[stream], (uint32_t)it & 1u);
-      ok = __all_sync(0xffffffffu, arrived);
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[2 * stream + h], (uint32_t)it & 1u));
       if (!ok) break;
       tc_fence_after();
-      // the first half's scores are under way while the tile's scales and
-      // masks are fetched, the second half's while the first's maximum is taken
-      uint32_t x[4][32];
-      tmem_ld_32x32b_x32(ts, x[0]);
-      tmem_ld_32x32b_x32(ts + 32, x[1]);
+      const uint32_t tsh = ts + h * 64;
+      // the scores are under way while their scales and masks are fetched
+      uint32_t x[2][32];
+      tmem_ld_32x32b_x32(tsh, x[0]);
+      tmem_ld_32x32b_x32(tsh + 32, x[1]);
       const TileMeta &tm = meta[j % kCaMeta];
-      uint32_t mask[4];
-      bool full = true;
+      uint32_t mask[2];
       // t = S * cf: cf at least the smallest normal number, so that a masked -inf stays one
-      float cf[4], lv[4];
+      float cf[2], lv[2];
+      const int before = sees - ((k.t0 + j) * kCaTile + 64 * h);   // positions of this half that the row sees
       #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int n = sees - ((k.t0 + j) * kCaTile + 32 * c);
+      for (int c = 0; c < 2; ++c) {
+        const int n = before - 32 * c;
         const uint32_t causal = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-        mask[c] = tm.valid[c] & causal;
-        full = full && mask[c] == 0xffffffffu;
-        cf[c] = fmaxf(tm.kref[c] * rowfac, 0x1p-126f);
-        lv[c] = tm.lv[c];
+        mask[c] = tm.valid[2 * h + c] & causal;
+        cf[c] = fmaxf(tm.kref[2 * h + c] * rowfac, 0x1p-126f);
+        lv[c] = tm.lv[2 * h + c];
       }
-      full = __all_sync(0xffffffffu, full);
+      const bool full = __all_sync(0xffffffffu, (mask[0] & mask[1]) == 0xffffffffu);
       tmem_wait_ld();
       arrived32(x[0]);
       arrived32(x[1]);
-      tmem_ld_32x32b_x32(ts + 64, x[2]);
-      tmem_ld_32x32b_x32(ts + 96, x[3]);
-      auto hide = [&](int c) {
+      if (!full) {
         #pragma unroll
-        for (int i = 0; i < 32; ++i) x[c][i] = (mask[c] >> i) & 1u ? x[c][i] : 0xFF800000u;
-      };
-      auto largest = [&](int c) {
-        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
+        for (int c = 0; c < 2; ++c) {
           #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            m[e] = fmaxf(fmaxf(m[e], __uint_as_float(x[c][i + 2 * e])), __uint_as_float(x[c][i + 2 * e + 1]));
+          for (int i = 0; i < 32; ++i) x[c][i] = (mask[c] >> i) & 1u ? x[c][i] : 0xFF800000u;
         }
-        return fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), cf[c], lv[c]);
-      };
-      if (!full) {
-        hide(0);
-        hide(1);
       }
-      // the tile's largest t + log2 vref
-      float top = fmaxf(largest(0), largest(1));
-      tmem_wait_ld();
-      arrived32(x[2]);
-      arrived32(x[3]);
-      if (!full) {
-        hide(2);
-        hide(3);
+      // the half's largest t + log2 vref
+      float top[2];
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float m0 = max3(x[c][0], x[c][1], x[c][2]), m1 = max3(x[c][3], x[c][4], x[c][5]);
+        #pragma unroll
+        for (int i = 6; i < 30; i += 4) {
+          m0 = max3(__float_as_uint(m0), x[c][i], x[c][i + 1]);
+          m1 = max3(__float_as_uint(m1), x[c][i + 2], x[c][i + 3]);
+        }
+        m0 = max3(__float_as_uint(m0), x[c][30], x[c][31]);
+        top[c] = fmaf(fmaxf(m0, m1), cf[c], lv[c]);
       }
-      top = fmaxf(top, fmaxf(largest(2), largest(3)));
-      const bool need = top > r + kCaLazy;
+      const float high = fmaxf(top[0], top[1]);
+      const bool need = high > r + kCaLazy;
       if (__any_sync(0xffffffffu, need)) {
-        const float f = need && r != -INFINITY ? ex2(r - top) : 1.0f;
-        if (need) r = top;
+        const float f = need && r != -INFINITY ? ex2(r - high) : 1.0f;
+        if (need) r = high;
         l *= f;
-        if (it > 0) {
+        if (u > 0) {
+          // the product of the half before has to be done
+          ok = __all_sync(0xffffffffu, mbar_wait(&o_done[2 * stream + (h ^ 1)], (uint32_t)((u - 1) >> 1) & 1u));
+          if (!ok) break;
+          tc_fence_after();
           #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t o[16];
@@ -769,7 +780,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       }
       const float rs = r == -INFINITY ? 0.0f : r;
       #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t y[16];
         const float bias = lv[c] - rs;
         const uint64_t cf2 = pack_f32x2(cf[c], cf[c]), b2 = pack_f32x2(bias, bias);
@@ -784,19 +795,19 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
           else sum0 = add_f32x2(sum0, pack_f32x2(a, b));
         }
         const float2 both = unpack_f32x2(add_f32x2(sum0, sum1));
-        l = fmaf(both.x + both.y, tm.inv_vref[c], l);
-        tmem_st_32x32b_x16(ts + 16 * c, y);
-        if (c & 1) {   // half of P' is there: its products can start
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * stream + (c >> 1)]);
-        }
+        l = fmaf(both.x + both.y, tm.inv_vref[2 * h + c], l);
+        tmem_st_32x32b_x16(tsh + 16 * c, y);
       }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[2 * stream + h]);
     }
-    if (ok && count > 0) ok = mbar_wait(&o_done[stream], 0);
-    // stream 1 hands its O over in the K ring: the other stream's products have to be done too
-    if (ok && !two && stream == 1 && count > 0) ok = mbar_wait(&o_done[0], 0);
+    // the last product is that of the last tile's second half
+    if (ok && count > 0) ok = mbar_wait(&o_done[2 * stream + 1], (uint32_t)(count - 1) & 1u);
+    // stream 1 hands its O over in the K ring: the other stream's products have
+    // to be done too (drain has one phase; o_done may be phases behind)
+    if (ok && !two && stream == 1 && count > 0) ok = mbar_wait(&drain[0], 0);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutChunk);
     tc_fence_after();
