@@ -25,8 +25,11 @@
 // With t = S * kref * qscale * log2 e, a weight is P' = 2^(t + log2 vref - r):
 // the reference r follows the largest t + log2 vref, so the f16 P' stays near
 // 1 however the value scales spread, and the sum of 2^(t - r) is that of P' /
-// vref.  r moves (and O, in tensor memory, is rescaled) only when a tile
-// exceeds it by more than 8, so P' < 2^8.  P' overwrites S in place.
+// vref.  r moves (and O, in tensor memory, is rescaled) only when the weights
+// of 64 positions, taken with the r of before, sum to 2^13 or more, which also
+// keeps each below f16's largest value: the common case needs no maximum at
+// all.  A row's first r is the maximum of its first 64 positions.  P' overwrites
+// S in place.
 // A tile goes through in halves of 64 positions, each with scores of its own in
 // tensor memory, so that a stream's products of one half run while its softmax
 // works on the other, and both streams' softmaxes never wait for theirs.  A CTA with 128
@@ -62,16 +65,18 @@ constexpr int kCaTile = 128;      // positions a tile
 constexpr int kCaStages = 2;      // stages of the K ring and of the V ring
 constexpr int kCaMeta = 8;        // tiles whose scales are kept (more than the stages ahead of the softmax)
 constexpr uint32_t kStatusTimeoutChunk = 1u << 4;
-constexpr float kCaLazy = 8.0f;   // r moves when a row's maximum exceeds it by this
+constexpr float kCaMost = 8192.0f;   // r moves when a row's weights of 64 positions reach this sum
 constexpr int kCaMaxSplits = 64;
 
-// What the softmax needs of a tile, for each 32 positions.
+// What the softmax needs of a tile: for each of its two halves of 64 positions
+// and the 32-position parts of a half
 struct TileMeta {
-  float kref[4];
-  float lv[4];        // log2 vref
-  float inv_vref[4];
-  uint32_t valid[4];  // bit i: the position is in the cache
-  uint32_t nan[4];    // bit i: the position's value vector is not finite (diagonal tiles only)
+  struct Half {
+    float kref[2], lv[2];                   // lv = log2 vref
+    float inv_vref[2];
+    uint32_t valid[2];                      // bit i: the position is in the cache
+  } half[2];
+  uint32_t nan[4];                          // bit i: the position's value vector is not finite (diagonal tiles only)
 };
 
 struct ChunkArgs {
@@ -85,6 +90,8 @@ struct ChunkArgs {
   int block_size, max_blocks, max_context;
   uint64_t bs_magic;            // ceil(2^64 / block_size)
   int64_t num_slots;
+  uint32_t num_blocks;
+  int tile_blocks, tile_rest;    // kCaTile = tile_blocks * block_size + tile_rest
   int splits, split_tiles;
   float scale_log2;
   float *part_ml, *part_acc;
@@ -217,12 +224,6 @@ __device__ __forceinline__ float ld_scale(const float *ptr) {
   return v;
 }
 
-__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
-  return r;
-}
-
 // Ties loaded registers to the wait before: nothing that reads them moves above it.
 __device__ __forceinline__ void arrived32(uint32_t (&r)[32]) {
   #pragma unroll
@@ -246,6 +247,20 @@ __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn_major) {
 // atoms of 64 f16 (128-byte swizzled rows), 16 KB apart.
 __device__ __forceinline__ int piece_off(int r, int c) {
   return (c >> 3) * (kCaRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// Shared memory by its own addresses (a pointer made from an aligned base would
+// be a generic one).
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t at, uint32_t a) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(a) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
 }
 
 // What a CTA works on.
@@ -404,28 +419,38 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     const int row_in = D == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) : lane >> 2;
     const int piece = D == 128 ? ((lane >> 3) & 1) * 4 + (lane & 3) : lane & 3;
     const int32_t *table = p.block_tables + (int64_t)k.b * p.max_blocks;
-    // the slot of this lane's position of local tile j (-1: not read)
-    auto slot_of = [&](int j) -> int {
-      const int pos = (k.t0 + j) * kCaTile + 32 * cw + lane;
-      if (j >= k.tiles || pos >= k.kv_end) return -1;
-      const int bi = (int)__umul64hi((uint64_t)pos, p.bs_magic);
-      if (bi >= p.max_blocks) return -1;
-      const int blk = __ldg(table + bi);
-      const int64_t sl = (int64_t)blk * p.block_size + (pos - bi * p.block_size);
-      return blk < 0 || sl >= p.num_slots ? -1 : (int)sl;
+    // This lane's position of each tile, walked tile by tile: its block in the
+    // table and its place in it.  fetch() loads the block of the next tile;
+    // slot() says where that is, -1 where nothing is read.  A tile lies
+    // between the two, so that nothing waits for the table.
+    int pos = k.t0 * kCaTile + 32 * cw + lane;
+    int bi = (int)__umul64hi((uint64_t)pos, p.bs_magic), in_block = pos - bi * p.block_size;
+    int blk = 0, at = 0;
+    bool there = false;
+    auto fetch = [&]() {
+      there = pos < k.kv_end && bi < p.max_blocks;
+      blk = __ldg(table + min(bi, p.max_blocks - 1));
+      at = in_block;
+      pos += kCaTile;
+      bi += p.tile_blocks;
+      in_block += p.tile_rest;
+      if (in_block >= p.block_size) {
+        in_block -= p.block_size;
+        ++bi;
+      }
     };
+    auto slot_of = [&]() -> int { return there && (uint32_t)blk < p.num_blocks ? blk * p.block_size + at : -1; };
     const uint8_t *codes = (is_k ? p.kc : p.vc) + kvh * D + piece * 16;
-    const int row_bytes = p.Hkv * D;
+    const uint32_t row_bytes = (uint32_t)(p.Hkv * D);
     // A position that is not in the cache reads slot 0 instead (a load with no
     // condition: a select behind it would wait for it).  Its key is masked by
     // the softmax whatever it holds, its value is zeroed, its scales are
     // dropped where they are used.
     auto load_codes = [&](int slot, uint4 (&r)[STEPS]) {
+      const int s = max(slot, 0);
       #pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const int s = __shfl_sync(0xffffffffu, slot, i * RP + row_in);
-        r[i] = ld_codes(codes + (int64_t)max(s, 0) * row_bytes);
-      }
+      for (int i = 0; i < STEPS; ++i)
+        r[i] = ld_codes(codes + (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, s, i * RP + row_in) * row_bytes);
     };
     auto load_scale = [&](const float *scales, int slot) {
       return ld_scale(scales + (int64_t)max(slot, 0) * p.Hkv + kvh);
@@ -459,10 +484,20 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     };
     // 2^-x of a power of two 2^x
     auto inverse = [](uint32_t bits) { return __uint_as_float((254u << 23) - bits); };
-    // 16 codes of row r as f16
-    auto store = [&](uint8_t *dst, int r, const uint32_t (&h)[8]) {
-      *reinterpret_cast<uint4 *>(dst + piece_off(r, 2 * piece)) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4 *>(dst + piece_off(r, 2 * piece + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+    // Where this lane's two 16-byte pieces of its row of step i go, relative to
+    // the warp's rows of a stage: the step's rows are whole 8-row groups on
+    // (D = 64), or half ones (D = 128: the swizzle's bit 2 alternates).
+    uint32_t put[2][2];
+    #pragma unroll
+    for (int odd = 0; odd < 2; ++odd) {
+      #pragma unroll
+      for (int c = 0; c < 2; ++c)
+        put[odd][c] = (uint32_t)piece_off(32 * cw + row_in + odd * RP, 2 * piece + c) - odd * RP * 128;
+    }
+    auto store = [&](uint32_t stage, int i, const uint32_t (&h)[8]) {
+      const uint32_t to = stage + i * RP * 128;
+      sts128(to + put[i & 1][0], h[0], h[1], h[2], h[3]);
+      sts128(to + put[i & 1][1], h[4], h[5], h[6], h[7]);
     };
     // stage j % kCaStages is free (its products of kCaStages tiles ago are done)
     auto wait_free = [&](uint64_t *empty, int j) -> bool {
@@ -476,7 +511,9 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     };
 
     uint4 r[STEPS];
-    int slot = slot_of(0), next = slot_of(1);
+    fetch();
+    int slot = slot_of();
+    fetch();
     float vsc = load_scale(p.vs, slot);
     bool ok = true;
     if (is_k) {
@@ -484,7 +521,8 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       load_codes(slot, r);
       #pragma unroll 1
       for (int j = 0; j < k.tiles; ++j) {
-        const int after = slot_of(j + 2);
+        const int next = slot_of();
+        fetch();
         // K' = code * ks / kref, and what the softmax needs of the tile's scales
         const float scale = slot >= 0 ? ksc : 0.0f;
         const uint32_t kb = reference(scale, 0), vb = reference(value_scale(vsc, slot), 6);
@@ -495,17 +533,16 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         ok = wait_free(k_empty, j);
         if (!ok) break;
         if (lane == 0) {
-          TileMeta &t = meta[j % kCaMeta];
-          t.kref[cw] = __uint_as_float(kb);
-          t.valid[cw] = valid;
-          t.lv[cw] = (float)((int)(vb >> 23) - 127);
-          t.inv_vref[cw] = inverse(vb);
+          const uint32_t m = smem_u32(&meta[j % kCaMeta].half[cw >> 1]) + (cw & 1) * 4;
+          sts32(m, kb);
+          sts32(m + 8, __float_as_uint((float)((int)(vb >> 23) - 127)));
+          sts32(m + 16, __float_as_uint(inverse(vb)));
+          sts32(m + 24, valid);
         }
-        uint8_t *dst = sm + S::K + (j % kCaStages) * S::kOperand;
+        const uint32_t stage = smem_u32(sm + S::K) + (j % kCaStages) * S::kOperand;
         #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-          const int row = i * RP + row_in;
-          const uint32_t f = __shfl_sync(0xffffffffu, split2, row);
+          const uint32_t f = __shfl_sync(0xffffffffu, split2, i * RP + row_in);
           const uint32_t hi2 = __byte_perm(f, f, 0x1010), lo2 = __byte_perm(f, f, 0x3232);
           const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
           uint32_t h[8];
@@ -516,10 +553,9 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
             h[e] = fma_f16x2(a, hi2, mul_f16x2(a, lo2));
             h[e + 1] = fma_f16x2(b, hi2, mul_f16x2(b, lo2));
           }
-          store(dst, 32 * cw + row, h);
+          store(stage, i, h);
         }
         slot = next;
-        next = after;
         ksc = load_scale(p.ks, slot);
         vsc = load_scale(p.vs, slot);
         load_codes(slot, r);
@@ -529,11 +565,12 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       load_codes(slot, r);
       #pragma unroll 1
       for (int j = 0; j < k.tiles; ++j) {
-        const int after = slot_of(j + 2);
+        const int next = slot_of();
+        fetch();
         // V' = code * vs / vref
         const float scale = value_scale(vsc, slot);
         const float inv = inverse(reference(scale, 6));
-        const uint32_t ratio = f16_pair(scale * inv, scale * inv);
+        uint32_t ratio = f16_pair(scale * inv, scale * inv);
         const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
         if (valid != 0xffffffffu) {
           #pragma unroll
@@ -555,16 +592,15 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
             if (bad) r[i] = make_uint4(0u, 0u, 0u, 0u);
             nan |= __reduce_or_sync(0xffffffffu, bad ? 1u << (i * RP + row_in) : 0u);
           }
+          if ((nan >> lane) & 1u) ratio = 0u;
         }
         ok = wait_free(v_empty, j);
         if (!ok) break;
         if (partial && lane == 0) meta[j % kCaMeta].nan[cw] = nan;
-        uint8_t *dst = sm + S::V + (j % kCaStages) * S::kOperand;
+        const uint32_t stage = smem_u32(sm + S::V) + (j % kCaStages) * S::kOperand;
         #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-          const int row = i * RP + row_in;
-          uint32_t f = __shfl_sync(0xffffffffu, ratio, row);
-          if ((nan >> row) & 1u) f = 0u;
+          const uint32_t f = __shfl_sync(0xffffffffu, ratio, i * RP + row_in);
           const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
           uint32_t h[8];
           #pragma unroll
@@ -574,10 +610,9 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
             h[e] = mul_f16x2(a, f);
             h[e + 1] = mul_f16x2(b, f);
           }
-          store(dst, 32 * cw + row, h);
+          store(stage, i, h);
         }
         slot = next;
-        next = after;
         vsc = load_scale(p.vs, slot);
         load_codes(slot, r);
         publish(v_full, j);
@@ -706,6 +741,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     const int sees = has_row ? k.m - k.n + tok + 1 : 0x7FFFFFFF;
     float r = -INFINITY, l = 0.0f;
     bool ok = true;
+    const bool idle = !__any_sync(0xffffffffu, has_row);
     // half a tile, 64 positions, a turn
     #pragma unroll 1
     for (int u = 0; u < 2 * count; ++u) {
@@ -713,54 +749,76 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       const int j = two ? it : 2 * it + stream;
       ok = __all_sync(0xffffffffu, mbar_wait(&s_full[2 * stream + h], (uint32_t)it & 1u));
       if (!ok) break;
+      if (idle) {   // none of the warp's rows is a token's: their weights are never used
+        if (lane == 0) mbar_arrive(&p_full[2 * stream + h]);
+        continue;
+      }
       tc_fence_after();
       const uint32_t tsh = ts + h * 64;
-      // the scores are under way while their scales and masks are fetched
+      // the scores are under way while their scales are fetched
       uint32_t x[2][32];
       tmem_ld_32x32b_x32(tsh, x[0]);
       tmem_ld_32x32b_x32(tsh + 32, x[1]);
-      const TileMeta &tm = meta[j % kCaMeta];
-      uint32_t mask[2];
+      const uint32_t m = smem_u32(&meta[j % kCaMeta].half[h]);
+      const uint4 m0 = lds128(m), m1 = lds128(m + 16);
       // t = S * cf: cf at least the smallest normal number, so that a masked -inf stays one
-      float cf[2], lv[2];
+      const float cf[2] = {fmaxf(__uint_as_float(m0.x) * rowfac, 0x1p-126f),
+                           fmaxf(__uint_as_float(m0.y) * rowfac, 0x1p-126f)};
+      const float lv[2] = {__uint_as_float(m0.z), __uint_as_float(m0.w)};
       const int before = sees - ((k.t0 + j) * kCaTile + 64 * h);   // positions of this half that the row sees
-      #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int n = before - 32 * c;
-        const uint32_t causal = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-        mask[c] = tm.valid[2 * h + c] & causal;
-        cf[c] = fmaxf(tm.kref[2 * h + c] * rowfac, 0x1p-126f);
-        lv[c] = tm.lv[2 * h + c];
-      }
-      const bool full = __all_sync(0xffffffffu, (mask[0] & mask[1]) == 0xffffffffu);
+      const bool full = __all_sync(0xffffffffu, before >= 64 && (m1.z & m1.w) == 0xffffffffu);
       tmem_wait_ld();
       arrived32(x[0]);
       arrived32(x[1]);
       if (!full) {
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
+          const int n = before - 32 * c;
+          const uint32_t mask = (c == 0 ? m1.z : m1.w) & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
           #pragma unroll
-          for (int i = 0; i < 32; ++i) x[c][i] = (mask[c] >> i) & 1u ? x[c][i] : 0xFF800000u;
+          for (int i = 0; i < 32; ++i) x[c][i] = (mask >> i) & 1u ? x[c][i] : 0xFF800000u;
         }
       }
-      // the half's largest t + log2 vref
-      float top[2];
-      #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float m0 = max3(x[c][0], x[c][1], x[c][2]), m1 = max3(x[c][3], x[c][4], x[c][5]);
+      // P' with the reference as it is, and its sums by 32 positions
+      float sum[2];
+      auto weights = [&]() {
+        const float rs = r == -INFINITY ? 0.0f : r;
         #pragma unroll
-        for (int i = 6; i < 30; i += 4) {
-          m0 = max3(__float_as_uint(m0), x[c][i], x[c][i + 1]);
-          m1 = max3(__float_as_uint(m1), x[c][i + 2], x[c][i + 3]);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t y[16];
+          const float bias = lv[c] - rs;
+          const uint64_t cf2 = pack_f32x2(cf[c], cf[c]), b2 = pack_f32x2(bias, bias);
+          uint64_t sum0 = 0, sum1 = 0;
+          #pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 t = unpack_f32x2(
+                fma_f32x2(pack_f32x2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), cf2, b2));
+            const float a = ex2(t.x), b = ex2(t.y);
+            y[i] = f16_pair(a, b);
+            if (i & 1) sum1 = add_f32x2(sum1, pack_f32x2(a, b));
+            else sum0 = add_f32x2(sum0, pack_f32x2(a, b));
+          }
+          const float2 both = unpack_f32x2(add_f32x2(sum0, sum1));
+          sum[c] = both.x + both.y;
+          tmem_st_32x32b_x16(tsh + 16 * c, y);
         }
-        m0 = max3(__float_as_uint(m0), x[c][30], x[c][31]);
-        top[c] = fmaf(fmaxf(m0, m1), cf[c], lv[c]);
-      }
-      const float high = fmaxf(top[0], top[1]);
-      const bool need = high > r + kCaLazy;
-      if (__any_sync(0xffffffffu, need)) {
-        const float f = need && r != -INFINITY ? ex2(r - high) : 1.0f;
-        if (need) r = high;
+      };
+      weights();
+      // A row without a reference, or with weights too large for it (NaN too)?
+      // Then the half's largest t + log2 vref becomes the reference, O follows,
+      // and the weights are taken again: nothing has read them yet.
+      if (__any_sync(0xffffffffu, r == -INFINITY || !(sum[0] + sum[1] < kCaMost))) {
+        float high = -INFINITY;
+        #pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = -INFINITY;
+          #pragma unroll
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(x[c][i]));
+          high = fmaxf(high, fmaf(top, cf[c], lv[c]));
+        }
+        const bool move = high > r && (r == -INFINITY || !(sum[0] + sum[1] < kCaMost));
+        const float f = move && r != -INFINITY ? ex2(r - high) : 1.0f;
+        if (move) r = high;
         l *= f;
         if (u > 0) {
           // the product of the half before has to be done
@@ -777,27 +835,9 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
             tmem_st_32x32b_x16(to + 16 * c, o);
           }
         }
+        weights();
       }
-      const float rs = r == -INFINITY ? 0.0f : r;
-      #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t y[16];
-        const float bias = lv[c] - rs;
-        const uint64_t cf2 = pack_f32x2(cf[c], cf[c]), b2 = pack_f32x2(bias, bias);
-        uint64_t sum0 = 0, sum1 = 0;
-        #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 t = unpack_f32x2(
-              fma_f32x2(pack_f32x2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), cf2, b2));
-          const float a = ex2(t.x), b = ex2(t.y);
-          y[i] = f16_pair(a, b);
-          if (i & 1) sum1 = add_f32x2(sum1, pack_f32x2(a, b));
-          else sum0 = add_f32x2(sum0, pack_f32x2(a, b));
-        }
-        const float2 both = unpack_f32x2(add_f32x2(sum0, sum1));
-        l = fmaf(both.x + both.y, tm.inv_vref[2 * h + c], l);
-        tmem_st_32x32b_x16(tsh + 16 * c, y);
-      }
+      l = fmaf(sum[0], __uint_as_float(m1.x), fmaf(sum[1], __uint_as_float(m1.y), l));
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -854,7 +894,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         for (int c = 0; c < 4; ++c) {
           const int n = sees - ((k.t0 + j) * kCaTile + 32 * c);
           const uint32_t causal = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-          if (tm.nan[c] & tm.valid[c] & causal) l = __uint_as_float(0x7FC00000u);
+          if (tm.nan[c] & tm.half[c >> 1].valid[c & 1] & causal) l = __uint_as_float(0x7FC00000u);
         }
       }
       const int64_t oh = (int64_t)(k.first_q + tok) * p.Hq + kvh * p.G + head;
@@ -1034,6 +1074,9 @@ cudaError_t launch_chunk_attention(const ChunkAttention &a, cudaStream_t st) {
   // every pos < 2^32: the product exceeds pos / block_size by less than 2^-32
   p.bs_magic = ~0ull / (uint64_t)a.block_size + 1;
   p.num_slots = a.num_slots;
+  p.num_blocks = (uint32_t)(a.num_slots / a.block_size);
+  p.tile_blocks = kCaTile / a.block_size;
+  p.tile_rest = kCaTile % a.block_size;
   p.splits = c.splits;
   p.split_tiles = c.split_tiles;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
