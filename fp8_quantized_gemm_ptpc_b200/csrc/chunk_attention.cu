@@ -65,7 +65,8 @@ constexpr int kCaTile = 128;      // positions a tile
 constexpr int kCaStages = 2;      // stages of the K ring and of the V ring
 constexpr int kCaMeta = 8;        // tiles whose scales are kept (more than the stages ahead of the softmax)
 constexpr uint32_t kStatusTimeoutChunk = 1u << 4;
-constexpr float kCaMost = 8192.0f;   // r moves when a row's weights of 64 positions reach this sum
+constexpr float kCaMost = 8192.0f;   // r is looked at again when a row's weights of 64 positions reach this sum,
+constexpr float kCaLazy = 6.0f;      // and moves where the largest exceeds it by this (64 * 2^6 < kCaMost)
 constexpr int kCaMaxSplits = 64;
 
 // What the softmax needs of a tile: for each of its two halves of 64 positions
@@ -118,6 +119,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ void ex2_in_order(float &x) { asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(x)); }
+
 __device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -139,6 +142,15 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ void add_f32x2_in_order(uint64_t &a, uint64_t b) {
+  asm volatile("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+}
+
+__device__ __forceinline__ uint32_t f16_pair_in_order(float lo, float hi) {
+  uint32_t r;
+  asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -200,6 +212,16 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, u
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -222,6 +244,36 @@ __device__ __forceinline__ float ld_scale(const float *ptr) {
   float v;
   asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(ptr));
   return v;
+}
+
+// Waits for a phase, in few instructions; false after some seconds (a failed
+// try takes from tens to some thousand cycles).
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t left = 1u << 20;
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "AGAIN%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%2], %3;\n\t"
+      "@p bra THERE%=;\n\t"
+      "sub.u32 %1, %1, 1;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "@q bra AGAIN%=;\n\t"
+      "THERE%=:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done), "+r"(left)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// Of a stream's units, where it has every other tile, those that lie whole
+// within the first `seen` positions.
+__device__ __forceinline__ int plain_units(int seen, int stream) {
+  const int all = max(seen, 0) >> 6;              // units of both streams
+  const int tiles = all >> 1;                     // whole tiles, then perhaps half of one
+  const int mine = (tiles + 1 - stream) >> 1;
+  return 2 * mine + ((all & 1) && (tiles & 1) == stream ? 1 : 0);
 }
 
 // Ties loaded registers to the wait before: nothing that reads them moves above it.
@@ -510,113 +562,83 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       if (lane == 0) mbar_arrive(&full[j % kCaStages]);
     };
 
+    // One loop for both, so that the roles' code stays within the instruction
+    // cache (32 KB: beyond it, they run at half the rate).
+    uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+    const uint32_t ring = smem_u32(sm + (is_k ? S::K : S::V));
     uint4 r[STEPS];
     fetch();
     int slot = slot_of();
     fetch();
-    float vsc = load_scale(p.vs, slot);
+    float ksc = load_scale(p.ks, slot), vsc = load_scale(p.vs, slot);
+    load_codes(slot, r);
     bool ok = true;
-    if (is_k) {
-      float ksc = load_scale(p.ks, slot);
-      load_codes(slot, r);
-      #pragma unroll 1
-      for (int j = 0; j < k.tiles; ++j) {
-        const int next = slot_of();
-        fetch();
-        // K' = code * ks / kref, and what the softmax needs of the tile's scales
-        const float scale = slot >= 0 ? ksc : 0.0f;
-        const uint32_t kb = reference(scale, 0), vb = reference(value_scale(vsc, slot), 6);
-        const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
-        const float ratio = scale * inverse(kb);
-        const float hi = __half2float(__float2half_rn(ratio));
-        const uint32_t split2 = f16_pair(hi, ratio - hi);   // infinite scales: NaN, in their column alone
-        ok = wait_free(k_empty, j);
-        if (!ok) break;
-        if (lane == 0) {
+    #pragma unroll 1
+    for (int j = 0; j < k.tiles; ++j) {
+      const int next = slot_of();
+      fetch();
+      const float v_scale = value_scale(vsc, slot);
+      const float scale = is_k ? (slot >= 0 ? ksc : 0.0f) : v_scale;
+      const uint32_t vb = reference(v_scale, 6), ref = is_k ? reference(scale, 0) : vb;
+      const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
+      // x' = code * scale / ref, the ratio as a sum of two f16
+      const float ratio = scale * inverse(ref);
+      const float hi = __half2float(__float2half_rn(ratio));
+      uint32_t split2 = f16_pair(hi, ratio - hi);   // of an infinite scale: NaN (K: in its column alone)
+      uint32_t nan = 0;
+      // tiles that some rows see in part: P' = 0 must cancel a value that is
+      // not finite, so its vector is zeroed and marked for the rows that see it
+      const bool partial = !is_k && (k.t0 + j + 1) * kCaTile > all_see;
+      if (__builtin_expect(partial || (!is_k && valid != 0xffffffffu), 0)) {
+        nan = __ballot_sync(0xffffffffu, !(scale < INFINITY));
+        #pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+          const int row = i * RP + row_in;
+          bool bad = false;
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) bad = bad || (((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+          const bool there = (valid >> row) & 1u;
+          bad = bad && partial && there;
+          if (bad || !there) r[i] = make_uint4(0u, 0u, 0u, 0u);
+          nan |= __reduce_or_sync(0xffffffffu, bad ? 1u << row : 0u);
+        }
+        if (partial && ((nan >> lane) & 1u)) split2 = 0u;
+      }
+      ok = wait_free(empty, j);
+      if (!ok) break;
+      if (lane == 0) {
+        if (is_k) {
           const uint32_t m = smem_u32(&meta[j % kCaMeta].half[cw >> 1]) + (cw & 1) * 4;
-          sts32(m, kb);
+          sts32(m, ref);
           sts32(m + 8, __float_as_uint((float)((int)(vb >> 23) - 127)));
           sts32(m + 16, __float_as_uint(inverse(vb)));
           sts32(m + 24, valid);
+        } else if (partial) {
+          meta[j % kCaMeta].nan[cw] = nan;
         }
-        const uint32_t stage = smem_u32(sm + S::K) + (j % kCaStages) * S::kOperand;
-        #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-          const uint32_t f = __shfl_sync(0xffffffffu, split2, i * RP + row_in);
-          const uint32_t hi2 = __byte_perm(f, f, 0x1010), lo2 = __byte_perm(f, f, 0x3232);
-          const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-          uint32_t h[8];
-          #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            uint32_t a, b;
-            e4m3_f16x4(w[e >> 1], a, b);
-            h[e] = fma_f16x2(a, hi2, mul_f16x2(a, lo2));
-            h[e + 1] = fma_f16x2(b, hi2, mul_f16x2(b, lo2));
-          }
-          store(stage, i, h);
-        }
-        slot = next;
-        ksc = load_scale(p.ks, slot);
-        vsc = load_scale(p.vs, slot);
-        load_codes(slot, r);
-        publish(k_full, j);
       }
-    } else {
+      const uint32_t stage = ring + (j % kCaStages) * S::kOperand;
+      #pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const uint32_t f = __shfl_sync(0xffffffffu, split2, i * RP + row_in);
+        const uint32_t hi2 = __byte_perm(f, f, 0x1010), lo2 = __byte_perm(f, f, 0x3232);
+        const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+        uint32_t h[8];
+        #pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          uint32_t a, b;
+          e4m3_f16x4(w[e >> 1], a, b);
+          h[e] = fma_f16x2(a, hi2, mul_f16x2(a, lo2));
+          h[e + 1] = fma_f16x2(b, hi2, mul_f16x2(b, lo2));
+        }
+        store(stage, i, h);
+      }
+      slot = next;
+      ksc = load_scale(p.ks, slot);
+      vsc = load_scale(p.vs, slot);
       load_codes(slot, r);
-      #pragma unroll 1
-      for (int j = 0; j < k.tiles; ++j) {
-        const int next = slot_of();
-        fetch();
-        // V' = code * vs / vref
-        const float scale = value_scale(vsc, slot);
-        const float inv = inverse(reference(scale, 6));
-        uint32_t ratio = f16_pair(scale * inv, scale * inv);
-        const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
-        if (valid != 0xffffffffu) {
-          #pragma unroll
-          for (int i = 0; i < STEPS; ++i)
-            if (!((valid >> (i * RP + row_in)) & 1u)) r[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        // tiles that some rows see in part: P' = 0 must cancel a value that is
-        // not finite, so its vector is zeroed and marked for the rows that see it
-        uint32_t nan = 0;
-        const bool partial = (k.t0 + j + 1) * kCaTile > all_see;
-        if (partial) {
-          nan = __ballot_sync(0xffffffffu, !(scale < INFINITY));
-          #pragma unroll
-          for (int i = 0; i < STEPS; ++i) {
-            const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-            bool bad = false;
-            #pragma unroll
-            for (int e = 0; e < 4; ++e) bad = bad || (((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-            if (bad) r[i] = make_uint4(0u, 0u, 0u, 0u);
-            nan |= __reduce_or_sync(0xffffffffu, bad ? 1u << (i * RP + row_in) : 0u);
-          }
-          if ((nan >> lane) & 1u) ratio = 0u;
-        }
-        ok = wait_free(v_empty, j);
-        if (!ok) break;
-        if (partial && lane == 0) meta[j % kCaMeta].nan[cw] = nan;
-        const uint32_t stage = smem_u32(sm + S::V) + (j % kCaStages) * S::kOperand;
-        #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-          const uint32_t f = __shfl_sync(0xffffffffu, ratio, i * RP + row_in);
-          const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-          uint32_t h[8];
-          #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            uint32_t a, b;
-            e4m3_f16x4(w[e >> 1], a, b);
-            h[e] = mul_f16x2(a, f);
-            h[e + 1] = mul_f16x2(b, f);
-          }
-          store(stage, i, h);
-        }
-        slot = next;
-        vsc = load_scale(p.vs, slot);
-        load_codes(slot, r);
-        publish(v_full, j);
-      }
+      publish(full, j);
     }
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutChunk);
   } else if (stream == 4) {
@@ -741,107 +763,143 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     const int sees = has_row ? k.m - k.n + tok + 1 : 0x7FFFFFFF;
     float r = -INFINITY, l = 0.0f;
     bool ok = true;
-    const bool idle = !__any_sync(0xffffffffu, has_row);
-    // half a tile, 64 positions, a turn
-    #pragma unroll 1
-    for (int u = 0; u < 2 * count; ++u) {
-      const int it = u >> 1, h = u & 1;
-      const int j = two ? it : 2 * it + stream;
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[2 * stream + h], (uint32_t)it & 1u));
-      if (!ok) break;
-      if (idle) {   // none of the warp's rows is a token's: their weights are never used
-        if (lane == 0) mbar_arrive(&p_full[2 * stream + h]);
-        continue;
-      }
-      tc_fence_after();
-      const uint32_t tsh = ts + h * 64;
-      // the scores are under way while their scales are fetched
-      uint32_t x[2][32];
-      tmem_ld_32x32b_x32(tsh, x[0]);
-      tmem_ld_32x32b_x32(tsh + 32, x[1]);
-      const uint32_t m = smem_u32(&meta[j % kCaMeta].half[h]);
+    const int units = 2 * count;   // of 64 positions, two a tile
+    auto tile = [&](int u) { return two ? u >> 1 : (u & ~1) + stream; };
+    auto wait_scores = [&](int u) {
+      return __all_sync(0xffffffffu, bar_wait(&s_full[2 * stream + (u & 1)], (uint32_t)(u >> 1) & 1u));
+    };
+    uint32_t x[2][32], y[2][16];
+    float cf[2], lv[2], over[2], sum[2];
+    uint32_t valid[2];
+    // a unit's scores and what belongs to them
+    auto load = [&](int u) {
+      const uint32_t m = smem_u32(&meta[tile(u) % kCaMeta].half[u & 1]);
+      tmem_ld_32x32b_x32(ts + 64 * (u & 1), x[0]);
+      tmem_ld_32x32b_x32(ts + 64 * (u & 1) + 32, x[1]);
       const uint4 m0 = lds128(m), m1 = lds128(m + 16);
       // t = S * cf: cf at least the smallest normal number, so that a masked -inf stays one
-      const float cf[2] = {fmaxf(__uint_as_float(m0.x) * rowfac, 0x1p-126f),
-                           fmaxf(__uint_as_float(m0.y) * rowfac, 0x1p-126f)};
-      const float lv[2] = {__uint_as_float(m0.z), __uint_as_float(m0.w)};
-      const int before = sees - ((k.t0 + j) * kCaTile + 64 * h);   // positions of this half that the row sees
-      const bool full = __all_sync(0xffffffffu, before >= 64 && (m1.z & m1.w) == 0xffffffffu);
+      cf[0] = fmaxf(__uint_as_float(m0.x) * rowfac, 0x1p-126f);
+      cf[1] = fmaxf(__uint_as_float(m0.y) * rowfac, 0x1p-126f);
+      lv[0] = __uint_as_float(m0.z);
+      lv[1] = __uint_as_float(m0.w);
+      over[0] = __uint_as_float(m1.x);
+      over[1] = __uint_as_float(m1.y);
+      valid[0] = m1.z;
+      valid[1] = m1.w;
       tmem_wait_ld();
       arrived32(x[0]);
       arrived32(x[1]);
-      if (!full) {
+    };
+    // its weights with the reference as it is, and their sums by 32 positions
+    auto weights = [&]() {
+      const float rs = r == -INFINITY ? 0.0f : r;
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float bias = lv[c] - rs;
+        const uint64_t cf2 = pack_f32x2(cf[c], cf[c]), b2 = pack_f32x2(bias, bias);
+        uint64_t sum0 = 0, sum1 = 0;
+        // pair i's exponentials, then what pair i - 3 is for: written down in
+        // this order, since a warp issues in order and waits for each result
+        constexpr int kLag = 3;
+        float2 w[16];
         #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int n = before - 32 * c;
-          const uint32_t mask = (c == 0 ? m1.z : m1.w) & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
-          #pragma unroll
-          for (int i = 0; i < 32; ++i) x[c][i] = (mask >> i) & 1u ? x[c][i] : 0xFF800000u;
-        }
-      }
-      // P' with the reference as it is, and its sums by 32 positions
-      float sum[2];
-      auto weights = [&]() {
-        const float rs = r == -INFINITY ? 0.0f : r;
-        #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t y[16];
-          const float bias = lv[c] - rs;
-          const uint64_t cf2 = pack_f32x2(cf[c], cf[c]), b2 = pack_f32x2(bias, bias);
-          uint64_t sum0 = 0, sum1 = 0;
-          #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 t = unpack_f32x2(
-                fma_f32x2(pack_f32x2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), cf2, b2));
-            const float a = ex2(t.x), b = ex2(t.y);
-            y[i] = f16_pair(a, b);
-            if (i & 1) sum1 = add_f32x2(sum1, pack_f32x2(a, b));
-            else sum0 = add_f32x2(sum0, pack_f32x2(a, b));
+        for (int i = 0; i < 16 + kLag; ++i) {
+          if (i < 16) {
+            w[i] = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), cf2, b2));
+            ex2_in_order(w[i].x);
+            ex2_in_order(w[i].y);
           }
-          const float2 both = unpack_f32x2(add_f32x2(sum0, sum1));
-          sum[c] = both.x + both.y;
-          tmem_st_32x32b_x16(tsh + 16 * c, y);
-        }
-      };
-      weights();
-      // A row without a reference, or with weights too large for it (NaN too)?
-      // Then the half's largest t + log2 vref becomes the reference, O follows,
-      // and the weights are taken again: nothing has read them yet.
-      if (__any_sync(0xffffffffu, r == -INFINITY || !(sum[0] + sum[1] < kCaMost))) {
-        float high = -INFINITY;
-        #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float top = -INFINITY;
-          #pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(x[c][i]));
-          high = fmaxf(high, fmaf(top, cf[c], lv[c]));
-        }
-        const bool move = high > r && (r == -INFINITY || !(sum[0] + sum[1] < kCaMost));
-        const float f = move && r != -INFINITY ? ex2(r - high) : 1.0f;
-        if (move) r = high;
-        l *= f;
-        if (u > 0) {
-          // the product of the half before has to be done
-          ok = __all_sync(0xffffffffu, mbar_wait(&o_done[2 * stream + (h ^ 1)], (uint32_t)((u - 1) >> 1) & 1u));
-          if (!ok) break;
-          tc_fence_after();
-          #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld_32x32b_x16(to + 16 * c, o);
-            tmem_wait_ld();
-            #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st_32x32b_x16(to + 16 * c, o);
+          if (i >= kLag) {
+            const float2 v = w[i - kLag];
+            y[c][i - kLag] = f16_pair_in_order(v.x, v.y);
+            add_f32x2_in_order(i & 1 ? sum1 : sum0, pack_f32x2(v.x, v.y));
           }
         }
-        weights();
+        const float2 both = unpack_f32x2(add_f32x2(sum0, sum1));
+        sum[c] = both.x + both.y;
       }
-      l = fmaf(sum[0], __uint_as_float(m1.x), fmaf(sum[1], __uint_as_float(m1.y), l));
+    };
+    auto hand_over = [&](int u) {
+      l = fmaf(sum[0], over[0], fmaf(sum[1], over[1], l));
+      tmem_st_32x32b_x16(ts + 64 * (u & 1), y[0]);
+      tmem_st_32x32b_x16(ts + 64 * (u & 1) + 16, y[1]);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[2 * stream + h]);
+      if (lane == 0) mbar_arrive(&p_full[2 * stream + (u & 1)]);
+    };
+    if (!__any_sync(0xffffffffu, has_row)) {
+      // none of the warp's rows is a token's: their weights are never used
+      for (int u = 0; u < units && ok; ++u) {
+        ok = wait_scores(u);
+        if (ok && lane == 0) mbar_arrive(&p_full[2 * stream + (u & 1)]);
+      }
+    } else {
+      // units whose positions every row of the warp sees, by their place
+      const int plain = min(units, __reduce_min_sync(0xffffffffu, two ? (sees - k.t0 * kCaTile) >> 6
+                                                                      : plain_units(sees - k.t0 * kCaTile, stream)));
+      int u = 0;
+      #pragma unroll 1
+      while (u < units && ok) {
+        // A unit that may need anything: a mask, a first reference or another one.
+        ok = wait_scores(u);
+        if (!ok) break;
+        tc_fence_after();
+        load(u);
+        const int before = sees - ((k.t0 + tile(u)) * kCaTile + 64 * (u & 1));   // positions of it that the row sees
+        float high = -INFINITY;
+        #pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int n = before - 32 * c;
+          const uint32_t mask = valid[c] & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
+          float top = -INFINITY;
+          #pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            x[c][i] = (mask >> i) & 1u ? x[c][i] : 0xFF800000u;
+            top = fmaxf(top, __uint_as_float(x[c][i]));
+          }
+          high = fmaxf(high, fmaf(top, cf[c], lv[c]));
+        }
+        const bool move = high > r + kCaLazy;
+        if (__any_sync(0xffffffffu, move)) {
+          const float f = move && r != -INFINITY ? ex2(r - high) : 1.0f;
+          if (move) r = high;
+          l *= f;
+          if (u > 0) {
+            // O follows, once the product of the unit before is done
+            ok = __all_sync(0xffffffffu, bar_wait(&o_done[2 * stream + ((u - 1) & 1)], (uint32_t)((u - 1) >> 1) & 1u));
+            if (!ok) break;
+            tc_fence_after();
+            #pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {
+              uint32_t o[8];
+              tmem_ld_32x32b_x8(to + 8 * c, o);
+              tmem_wait_ld();
+              #pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_32x32b_x8(to + 8 * c, o);
+            }
+          }
+        }
+        weights();
+        hand_over(u);
+        ++u;
+        // Units that need nothing, in a loop of their own: little code without
+        // jumps.  Whether a unit was one shows when its weights are there; one
+        // that was not (a row without a reference, weights too large for the
+        // reference or NaN, a position that is not in the cache) goes back.
+        #pragma unroll 1
+        for (; u < plain; ++u) {
+          ok = wait_scores(u);
+          if (!ok) break;
+          tc_fence_after();
+          load(u);
+          weights();
+          if (__any_sync(0xffffffffu, r == -INFINITY || !(sum[0] + sum[1] < kCaMost) || (valid[0] & valid[1]) != 0xffffffffu))
+            break;
+          hand_over(u);
+        }
+      }
     }
     // the last product is that of the last tile's second half
     if (ok && count > 0) ok = mbar_wait(&o_done[2 * stream + 1], (uint32_t)(count - 1) & 1u);
