@@ -26,7 +26,7 @@
 // the reference r follows the largest t + log2 vref, so the f16 P' stays near
 // 1 however the value scales spread, and the sum of 2^(t - r) is that of P' /
 // vref.  r moves (and O, in tensor memory, is rescaled) only when the weights
-// of 64 positions, taken with the r of before, sum to 2^13 or more, which also
+// of 64 positions, taken with the r of before, sum to 2^15 or more, which also
 // keeps each below f16's largest value: the common case needs no maximum at
 // all.  A row's first r is the maximum of its first 64 positions.  P' overwrites
 // S in place.
@@ -65,8 +65,8 @@ constexpr int kCaTile = 128;      // positions a tile
 constexpr int kCaStages = 2;      // stages of the K ring and of the V ring
 constexpr int kCaMeta = 8;        // tiles whose scales are kept (more than the stages ahead of the softmax)
 constexpr uint32_t kStatusTimeoutChunk = 1u << 4;
-constexpr float kCaMost = 8192.0f;   // r is looked at again when a row's weights of 64 positions reach this sum,
-constexpr float kCaLazy = 6.0f;      // and moves where the largest exceeds it by this (64 * 2^6 < kCaMost)
+constexpr float kCaMost = 32768.0f;   // r is looked at again when a row's weights of 64 positions reach this sum,
+constexpr float kCaLazy = 8.0f;       // and moves where the largest exceeds it by this (64 * 2^8 < kCaMost)
 constexpr int kCaMaxSplits = 64;
 
 // What the softmax needs of a tile: for each of its two halves of 64 positions
@@ -212,16 +212,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, u
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -498,11 +488,8 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     // condition: a select behind it would wait for it).  Its key is masked by
     // the softmax whatever it holds, its value is zeroed, its scales are
     // dropped where they are used.
-    auto load_codes = [&](int slot, uint4 (&r)[STEPS]) {
-      const int s = max(slot, 0);
-      #pragma unroll
-      for (int i = 0; i < STEPS; ++i)
-        r[i] = ld_codes(codes + (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, s, i * RP + row_in) * row_bytes);
+    auto load_step = [&](int slot, int i) {   // the codes of step i; slot >= 0
+      return ld_codes(codes + (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, slot, i * RP + row_in) * row_bytes);
     };
     auto load_scale = [&](const float *scales, int slot) {
       return ld_scale(scales + (int64_t)max(slot, 0) * p.Hkv + kvh);
@@ -553,7 +540,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     };
     // stage j % kCaStages is free (its products of kCaStages tiles ago are done)
     auto wait_free = [&](uint64_t *empty, int j) -> bool {
-      const bool w = j < kCaStages || mbar_wait(&empty[j % kCaStages], (uint32_t)(j / kCaStages - 1) & 1u);
+      const bool w = j < kCaStages || bar_wait(&empty[j % kCaStages], (uint32_t)(j / kCaStages - 1) & 1u);
       return __all_sync(0xffffffffu, w);
     };
     auto publish = [&](uint64_t *full, int j) {
@@ -571,12 +558,16 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     int slot = slot_of();
     fetch();
     float ksc = load_scale(p.ks, slot), vsc = load_scale(p.vs, slot);
-    load_codes(slot, r);
+    #pragma unroll
+    for (int i = 0; i < STEPS; ++i) r[i] = load_step(max(slot, 0), i);
     bool ok = true;
     #pragma unroll 1
     for (int j = 0; j < k.tiles; ++j) {
-      const int next = slot_of();
+      // the next tile's scales, and below its codes as soon as their registers
+      // are free: memory has a whole tile's time to answer
+      const int next = slot_of(), next0 = max(next, 0);
       fetch();
+      const float next_ksc = load_scale(p.ks, next), next_vsc = load_scale(p.vs, next);
       const float v_scale = value_scale(vsc, slot);
       const float scale = is_k ? (slot >= 0 ? ksc : 0.0f) : v_scale;
       const uint32_t vb = reference(v_scale, 6), ref = is_k ? reference(scale, 0) : vb;
@@ -633,12 +624,12 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
           h[e + 1] = fma_f16x2(b, hi2, mul_f16x2(b, lo2));
         }
         store(stage, i, h);
+        r[i] = load_step(next0, i);
       }
-      slot = next;
-      ksc = load_scale(p.ks, slot);
-      vsc = load_scale(p.vs, slot);
-      load_codes(slot, r);
       publish(full, j);
+      slot = next;
+      ksc = next_ksc;
+      vsc = next_vsc;
     }
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutChunk);
   } else if (stream == 4) {
@@ -651,7 +642,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       const int s = warp - 16;
       const int count = two ? (s == 0 ? k.tiles0 : k.tiles) : (k.tiles + 1 - s) >> 1;
       auto wait_full = [&](uint64_t *bar, int j) {
-        return mbar_wait(&bar[j % kCaStages], (uint32_t)(j / kCaStages) & 1u);
+        return bar_wait(&bar[j % kCaStages], (uint32_t)(j / kCaStages) & 1u);
       };
       const uint32_t q_desc = desc_k_major(smem_u32(sm + S::Q)) + (two ? s : 0) * (S::kOperand >> 4);
       const uint32_t k_desc = desc_k_major(smem_u32(sm + S::K)), v_desc = desc_mn_major(smem_u32(sm + S::V));
@@ -679,7 +670,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         if (h == 1) mma_commit(&v_empty[j % kCaStages]);
       };
       auto tile = [&](int it) { return two ? it : 2 * it + s; };
-      bool ok = mbar_wait(q_full, 0);
+      bool ok = bar_wait(q_full, 0);
       if (ok && count > 0) {
         ok = wait_full(k_full, tile(0));
         tc_fence_after();
@@ -693,7 +684,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         ok = wait_full(v_full, j);
         #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          ok = ok && mbar_wait(&p_full[2 * s + h], (uint32_t)it & 1u);
+          ok = ok && bar_wait(&p_full[2 * s + h], (uint32_t)it & 1u);
           if (!ok) break;
           tc_fence_after();
           pv(j, h, it + h == 0);
@@ -715,7 +706,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       if (!ok) atomicOr(p.status, kStatusTimeoutChunk);
       // every product issued has completed before the CTA ends
       mma_commit(&drain[s]);
-      mbar_wait(&drain[s], 0);
+      bar_wait(&drain[s], 0);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -871,13 +862,17 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
             if (!ok) break;
             tc_fence_after();
             #pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) {
-              uint32_t o[8];
-              tmem_ld_32x32b_x8(to + 8 * c, o);
+            for (int c = 0; c < D / 32; ++c) {
+              tmem_ld_32x32b_x16(to + 32 * c, y[0]);
+              tmem_ld_32x32b_x16(to + 32 * c + 16, y[1]);
               tmem_wait_ld();
               #pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st_32x32b_x8(to + 8 * c, o);
+              for (int i = 0; i < 16; ++i) {
+                y[0][i] = __float_as_uint(__uint_as_float(y[0][i]) * f);
+                y[1][i] = __float_as_uint(__uint_as_float(y[1][i]) * f);
+              }
+              tmem_st_32x32b_x16(to + 32 * c, y[0]);
+              tmem_st_32x32b_x16(to + 32 * c + 16, y[1]);
             }
           }
         }
@@ -902,10 +897,10 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       }
     }
     // the last product is that of the last tile's second half
-    if (ok && count > 0) ok = mbar_wait(&o_done[2 * stream + 1], (uint32_t)(count - 1) & 1u);
+    if (ok && count > 0) ok = bar_wait(&o_done[2 * stream + 1], (uint32_t)(count - 1) & 1u);
     // stream 1 hands its O over in the K ring: the other stream's products have
     // to be done too (drain has one phase; o_done may be phases behind)
-    if (ok && !two && stream == 1 && count > 0) ok = mbar_wait(&drain[0], 0);
+    if (ok && !two && stream == 1 && count > 0) ok = bar_wait(&drain[0], 0);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutChunk);
     tc_fence_after();
