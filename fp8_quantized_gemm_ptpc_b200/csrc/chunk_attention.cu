@@ -266,6 +266,17 @@ __device__ __forceinline__ int plain_units(int seen, int stream) {
   return 2 * mine + ((all & 1) && (tiles & 1) == stream ? 1 : 0);
 }
 
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool bar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Ties loaded registers to the wait before: nothing that reads them moves above it.
 __device__ __forceinline__ void arrived32(uint32_t (&r)[32]) {
   #pragma unroll
@@ -760,14 +771,19 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       return __all_sync(0xffffffffu, bar_wait(&s_full[2 * stream + (u & 1)], (uint32_t)(u >> 1) & 1u));
     };
     uint32_t x[2][32], y[2][16];
+    uint4 m0, m1;
     float cf[2], lv[2], over[2], sum[2];
     uint32_t valid[2];
-    // a unit's scores and what belongs to them
-    auto load = [&](int u) {
+    // a unit's scores and what belongs to them, on their way
+    auto start = [&](int u) {
       const uint32_t m = smem_u32(&meta[tile(u) % kCaMeta].half[u & 1]);
       tmem_ld_32x32b_x32(ts + 64 * (u & 1), x[0]);
       tmem_ld_32x32b_x32(ts + 64 * (u & 1) + 32, x[1]);
-      const uint4 m0 = lds128(m), m1 = lds128(m + 16);
+      m0 = lds128(m);
+      m1 = lds128(m + 16);
+    };
+    // and here
+    auto arrive = [&]() {
       // t = S * cf: cf at least the smallest normal number, so that a masked -inf stays one
       cf[0] = fmaxf(__uint_as_float(m0.x) * rowfac, 0x1p-126f);
       cf[1] = fmaxf(__uint_as_float(m0.y) * rowfac, 0x1p-126f);
@@ -811,7 +827,6 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       }
     };
     auto hand_over = [&](int u) {
-      l = fmaf(sum[0], over[0], fmaf(sum[1], over[1], l));
       tmem_st_32x32b_x16(ts + 64 * (u & 1), y[0]);
       tmem_st_32x32b_x16(ts + 64 * (u & 1) + 16, y[1]);
       tmem_wait_st();
@@ -836,7 +851,8 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         ok = wait_scores(u);
         if (!ok) break;
         tc_fence_after();
-        load(u);
+        start(u);
+        arrive();
         const int before = sees - ((k.t0 + tile(u)) * kCaTile + 64 * (u & 1));   // positions of it that the row sees
         float high = -INFINITY;
         #pragma unroll
@@ -877,22 +893,39 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
           }
         }
         weights();
+        l = fmaf(sum[0], over[0], fmaf(sum[1], over[1], l));
         hand_over(u);
         ++u;
         // Units that need nothing, in a loop of their own: little code without
         // jumps.  Whether a unit was one shows when its weights are there; one
         // that was not (a row without a reference, weights too large for the
         // reference or NaN, a position that is not in the cache) goes back.
+        // The next unit's scores are mostly there by then: their barrier is
+        // tested (150 cycles) behind the exponentials, and they are fetched
+        // while P' is stored.
+        if (u >= plain) continue;
+        ok = wait_scores(u);
+        if (!ok) break;
+        tc_fence_after();
+        start(u);
         #pragma unroll 1
-        for (; u < plain; ++u) {
-          ok = wait_scores(u);
-          if (!ok) break;
-          tc_fence_after();
-          load(u);
+        while (true) {
+          arrive();
           weights();
-          if (__any_sync(0xffffffffu, r == -INFINITY || !(sum[0] + sum[1] < kCaMost) || (valid[0] & valid[1]) != 0xffffffffu))
-            break;
+          const bool more = u + 1 < plain;
+          const bool there = !more || bar_test(&s_full[2 * stream + ((u + 1) & 1)], (uint32_t)((u + 1) >> 1) & 1u);
+          const bool odd = r == -INFINITY || !(sum[0] + sum[1] < kCaMost) || (valid[0] & valid[1]) != 0xffffffffu;
+          if (__any_sync(0xffffffffu, odd || !there)) {
+            if (__any_sync(0xffffffffu, odd)) break;
+            ok = wait_scores(u + 1);
+            if (!ok) break;
+          }
+          l = fmaf(sum[0], over[0], fmaf(sum[1], over[1], l));
           hand_over(u);
+          ++u;
+          if (!more) break;
+          tc_fence_after();
+          start(u);
         }
       }
     }
@@ -1049,7 +1082,7 @@ ChunkPlan plan_chunk(int64_t total_q, int64_t B, int Hkv, int G, int64_t max_q, 
   c.split_tiles = (int)tiles;
   for (int64_t s = 1; s <= kCaMaxSplits; ++s) {
     const int64_t each = (tiles + s - 1) / s;
-    if (s > 1 && (each < 4 || ctas * s > 4 * sms)) break;
+    if (s > 1 && (each < 4 || ctas * s > 8 * sms)) break;
     const int64_t parts = (tiles + each - 1) / each;
     if (parts != s) continue;
     const int64_t cost = (ctas * s + sms - 1) / sms * (each + kFixed) + (s > 1 ? kFixed : 0);
