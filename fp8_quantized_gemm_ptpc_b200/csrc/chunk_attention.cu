@@ -340,8 +340,11 @@ __device__ __forceinline__ bool find_work(const ChunkArgs &p, int w, Work &k) {
   int before = 0;
   for (int base = 0; base < p.B; base += 32) {
     const int b = base + lane;
-    int first = 0, n = 0;
-    if (b < p.B) n = seq_tokens(p, b, first);
+    int first = 0, n = 0, m = 0;
+    if (b < p.B) {
+      m = max(__ldg(p.context_lens + b), 0);
+      n = seq_tokens(p, b, first);
+    }
     const int mine = (int)(((int64_t)n * p.G + 2 * kCaRows - 1) / (2 * kCaRows));
     int upto = mine;
     #pragma unroll
@@ -360,7 +363,7 @@ __device__ __forceinline__ bool find_work(const ChunkArgs &p, int w, Work &k) {
       const int tile = tiles - 1 - (w - start);
       k.row0 = tile * 2 * kCaRows;
       k.rows = (int)min((int64_t)2 * kCaRows, (int64_t)k.n * p.G - k.row0);
-      k.m = max(__ldg(p.context_lens + k.b), 0);
+      k.m = __shfl_sync(0xffffffffu, m, at);
       return true;
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
@@ -453,10 +456,15 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     tmem_relinquish();
   }
 
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_holder;
+  // The barriers and tensor memory are ready: each role passes here once its
+  // first loads are on their way.
+  auto all_set = [&]() -> uint32_t {
+    tc_fence_before();
+    asm volatile("bar.sync 4, %0;" ::"n"(kCaThreads) : "memory");
+    tc_fence_after();
+    return *reinterpret_cast<volatile uint32_t *>(tmem_holder);
+  };
+  uint32_t tmem_base;
 
   if (stream == 2 || stream == 3) {
     // ------------------------------------------------------------ converters
@@ -571,6 +579,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     float ksc = load_scale(p.ks, slot), vsc = load_scale(p.vs, slot);
     #pragma unroll
     for (int i = 0; i < STEPS; ++i) r[i] = load_step(max(slot, 0), i);
+    tmem_base = all_set();
     bool ok = true;
     #pragma unroll 1
     for (int j = 0; j < k.tiles; ++j) {
@@ -647,6 +656,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     // ------------------------------------------------------------ MMA issuers
     // A warp a stream, so that a stream's products wait for its own softmax alone.
     regs_down<kCaRegsIssuer>();
+    tmem_base = all_set();
     if (warp < 18 && elect_one()) {
       constexpr uint32_t idesc_qk = idesc_f16(kCaTile / 2, false);
       constexpr uint32_t idesc_pv = idesc_f16(D, true);
@@ -732,6 +742,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
                                                          (int64_t)(kvh * p.G + head) * D);
       #pragma unroll
       for (int c = 0; c < D / 8; ++c) w[c] = has_row ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      tmem_base = all_set();
       #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
