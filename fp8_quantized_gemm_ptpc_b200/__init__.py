@@ -171,6 +171,7 @@ def _check(fn: str, status: int):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(device: torch.device):
@@ -200,9 +201,10 @@ def _need_rows(t: torch.Tensor, name: str) -> int:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be a 2-d tensor with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return stride[0] if shape[0] > 1 else shape[1]
 
 
 class Workspace:
@@ -329,51 +331,64 @@ def _on_device(fn):
     launch goes to the current device; the stream is already that device's)."""
     @functools.wraps(fn)
     def call(*args, **kwargs):
-        dev = next((a.device for a in args if isinstance(a, torch.Tensor)), None)
-        if dev is None or not dev.type == "cuda" or dev.index == torch.cuda.current_device():
+        index = -1
+        for a in args or kwargs.values():
+            if isinstance(a, torch.Tensor):
+                index = a.get_device()
+                break
+        if index < 0 or index == _current_device():
             return fn(*args, **kwargs)
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             return fn(*args, **kwargs)
     return call
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _same_device(device: torch.device, *tensors):
+    index = device.index
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"the tensors are on {t.device} and on {device}")
+
+
+def _fresh(like: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def _norm_args(y, residual, pre_weight, post_weight, gate, h_out):
     ldr = _need_rows(residual, "residual")
-    T, C = residual.shape
-    ldy = 0
+    shape = residual.shape
+    T, C = shape
+    ldy = ldg = 0
     if y is not None:
         ldy = _need_rows(y, "y")
-        if y.shape != residual.shape:
+        if y.shape != shape:
             raise ValueError("y and residual differ in shape")
-    for name, w in (("pre_weight", pre_weight), ("post_weight", post_weight)):
-        if w is not None or name == "pre_weight":
-            _need(w, name, torch.bfloat16, 1)
-            if w.shape[0] != C:
-                raise ValueError(f"{name} must have {C} values")
-    ldg = 0
+    _need(pre_weight, "pre_weight", torch.bfloat16, 1)
+    if len(pre_weight) != C:
+        raise ValueError(f"pre_weight must have {C} values")
+    if post_weight is not None:
+        _need(post_weight, "post_weight", torch.bfloat16, 1)
+        if len(post_weight) != C:
+            raise ValueError(f"post_weight must have {C} values")
     if gate is not None:
         if isinstance(gate, torch.Tensor) and gate.dim() == 1:
             _need(gate, "gate", torch.bfloat16, 1)
-            if gate.shape[0] != C:
+            if len(gate) != C:
                 raise ValueError(f"gate must have {C} values")
         else:
             ldg = _need_rows(gate, "gate")
-            if gate.shape != residual.shape:
+            if gate.shape != shape:
                 raise ValueError("gate must be [C] or the shape of residual")
+    ldh = C
     if h_out is None:
-        h_out = torch.empty((T, C), dtype=torch.bfloat16, device=residual.device)
-    ldh = _need_rows(h_out, "h_out")
-    if h_out.shape != residual.shape:
-        raise ValueError("h_out and residual differ in shape")
-    _same_device(residual.device, y=y, pre_weight=pre_weight, post_weight=post_weight, gate=gate, h_out=h_out)
-    opt = lambda t: None if t is None else _ptr(t)  # noqa: E731
-    return h_out, (opt(y), ldy, _ptr(residual), ldr, opt(gate), ldg, opt(post_weight), _ptr(pre_weight), T, C), ldh
+        h_out = _fresh(residual)
+    else:
+        ldh = _need_rows(h_out, "h_out")
+        if h_out.shape != shape:
+            raise ValueError("h_out and residual differ in shape")
+    _same_device(residual.device, y, pre_weight, post_weight, gate, h_out)
+    return h_out, (None if y is None else _ptr(y), ldy, _ptr(residual), ldr, None if gate is None else _ptr(gate), ldg,
+                   None if post_weight is None else _ptr(post_weight), _ptr(pre_weight), T, C), ldh
 
 
 @_on_device
@@ -389,11 +404,13 @@ def residual_norm(y, residual, pre_weight, post_weight=None, gate=None, residual
     contiguous); weights bf16 [C]; gate bf16 [C] or [T, C].  y None: h is the
     residual (the first norm of a model).  h_out may be residual itself."""
     h_out, args, ldh = _norm_args(y, residual, pre_weight, post_weight, gate, h_out)
-    out = torch.empty(residual.shape, dtype=torch.bfloat16, device=residual.device) if out is None else out
-    _need(out, "out", torch.bfloat16, 2)
-    if out.shape != residual.shape:
-        raise ValueError("out and residual differ in shape")
-    _same_device(residual.device, out=out)
+    if out is None:
+        out = _fresh(residual)
+    else:
+        _need(out, "out", torch.bfloat16, 2)
+        if out.shape != residual.shape:
+            raise ValueError("out and residual differ in shape")
+        _same_device(residual.device, out)
     _check("ptpc_residual_norm",
            lib.ptpc_residual_norm(*args, float(eps), float(residual_scale), _ptr(h_out), ldh, _ptr(out),
                                   _stream(residual.device)))
@@ -407,14 +424,18 @@ def residual_norm_quantize(y, residual, pre_weight, post_weight=None, gate=None,
     """residual_norm with x as the per-token E4M3 codes and scales that
     scaled_mm reads -> (h bf16 [T, C], Xq uint8 [T, C], x_scale fp32 [T])."""
     h_out, args, ldh = _norm_args(y, residual, pre_weight, post_weight, gate, h_out)
-    T, C = residual.shape
-    Xq = torch.empty((T, C), dtype=torch.uint8, device=residual.device) if Xq is None else Xq
-    x_scale = torch.empty((T,), dtype=torch.float32, device=residual.device) if x_scale is None else x_scale
-    _need(Xq, "Xq", torch.uint8, 2)
-    _need(x_scale, "x_scale", torch.float32, 1)
-    if Xq.shape != residual.shape or x_scale.shape[0] != T:
+    shape = residual.shape
+    if Xq is None:
+        Xq = residual.new_empty(shape, dtype=torch.uint8)
+    else:
+        _need(Xq, "Xq", torch.uint8, 2)
+    if x_scale is None:
+        x_scale = residual.new_empty(shape[0], dtype=torch.float32)
+    else:
+        _need(x_scale, "x_scale", torch.float32, 1)
+    if Xq.shape != shape or len(x_scale) != shape[0]:
         raise ValueError("Xq or x_scale does not fit residual")
-    _same_device(residual.device, Xq=Xq, x_scale=x_scale)
+    _same_device(residual.device, Xq, x_scale)
     _check("ptpc_residual_norm_quantize",
            lib.ptpc_residual_norm_quantize(*args, float(eps), float(residual_scale), _ptr(h_out), ldh, _ptr(Xq),
                                            _ptr(x_scale), _stream(residual.device)))
@@ -718,9 +739,10 @@ def _need_heads(t: torch.Tensor, name: str) -> int:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1) or (stride[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"{name} must be a 3-d tensor with dense heads")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _need_cache(k_cache, v_cache, k_scale, v_scale):
@@ -729,9 +751,10 @@ def _need_cache(k_cache, v_cache, k_scale, v_scale):
     _need(v_cache, "v_cache", torch.uint8, 4)
     _need(k_scale, "k_scale", torch.float32, 3)
     _need(v_scale, "v_scale", torch.float32, 3)
-    if v_cache.shape != k_cache.shape or k_scale.shape != k_cache.shape[:3] or v_scale.shape != k_scale.shape:
+    shape, scales = k_cache.shape, k_scale.shape
+    if v_cache.shape != shape or scales != shape[:3] or v_scale.shape != scales:
         raise ValueError("shape mismatch")
-    return tuple(k_cache.shape)
+    return shape
 
 
 @_on_device
@@ -752,20 +775,22 @@ def rope_kv_cache_append(q, k, v, cos_sin, positions, slots, k_cache, v_cache, k
     _need(positions, "positions", torch.int64, 1)
     _need(slots, "slots", torch.int64, 1)
     nb, bs, Hkv, D = _need_cache(k_cache, v_cache, k_scale, v_scale)
-    T, Hq, _ = q.shape
-    if q.shape[2] != D or k.shape != (T, Hkv, D) or v.shape != k.shape or positions.shape[0] != T or \
-            slots.shape[0] != T:
+    T, Hq, Dq = q.shape
+    if Dq != D or k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D) or len(positions) != T or len(slots) != T:
         raise ValueError("shape mismatch")
-    q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
-    ldo = _need_heads(q_out, "q_out")
-    if q_out.shape != q.shape:
-        raise ValueError("q_out and q differ in shape")
-    _same_device(q.device, k=k, v=v, cos_sin=cos_sin, positions=positions, slots=slots, k_cache=k_cache,
-                 v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, q_out=q_out)
+    ldo = Hq * D
+    if q_out is None:
+        q_out = _fresh(q)
+    else:
+        ldo = _need_heads(q_out, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out and q differ in shape")
+    _same_device(q.device, k, v, cos_sin, positions, slots, k_cache, v_cache, k_scale, v_scale, q_out)
+    rows, turned = cos_sin.shape
     _check("ptpc_rope_kv_cache_append",
-           lib.ptpc_rope_kv_cache_append(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(cos_sin), cos_sin.shape[0],
-                                         cos_sin.shape[1], int(bool(interleaved)), _ptr(positions), _ptr(slots), T,
-                                         Hq, Hkv, D, bs, nb, _ptr(q_out), ldo, _ptr(k_cache), _ptr(v_cache),
+           lib.ptpc_rope_kv_cache_append(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(cos_sin), rows,
+                                         turned, int(bool(interleaved)), _ptr(positions), _ptr(slots), T, Hq, Hkv, D,
+                                         bs, nb, _ptr(q_out), ldo, _ptr(k_cache), _ptr(v_cache),
                                          _ptr(k_scale), _ptr(v_scale), _stream(q.device)))
     return q_out
 
@@ -825,16 +850,18 @@ def chunk_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, context
     _need(block_tables, "block_tables", torch.int32, 2)
     _need(context_lens, "context_lens", torch.int32, 1)
     _need(cu_q, "cu_q", torch.int32, 1)
-    total, Hq, _ = q.shape
-    B = context_lens.shape[0]
-    if q.shape[2] != D or Hq % Hkv or block_tables.shape[0] != B or cu_q.shape[0] != B + 1:
+    total, Hq, Dq = q.shape
+    B = len(context_lens)
+    tables, table_blocks = block_tables.shape
+    if Dq != D or Hq % max(Hkv, 1) or tables != B or len(cu_q) != B + 1:
         raise ValueError("shape mismatch")
-    out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
-    _need(out, "out", torch.bfloat16, 3)
-    if out.shape != q.shape:
-        raise ValueError("out and q differ in shape")
-    _same_device(q.device, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                 block_tables=block_tables, context_lens=context_lens, cu_q=cu_q, out=out)
+    if out is None:
+        out = _fresh(q)
+    else:
+        _need(out, "out", torch.bfloat16, 3)
+        if out.shape != q.shape:
+            raise ValueError("out and q differ in shape")
+    _same_device(q.device, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, cu_q, out)
     need = int(lib.ptpc_chunk_attention_workspace_size(total, B, Hq, Hkv, D, max_q, max_context))
     if ws is not None:
         ws.ensure(need)
@@ -845,6 +872,6 @@ def chunk_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, context
     _check("ptpc_chunk_attention",
            lib.ptpc_chunk_attention(_ptr(q), ldq, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
                                     _ptr(block_tables), _ptr(context_lens), _ptr(cu_q), total, B, max_q, Hq, Hkv, D,
-                                    bs, nb, block_tables.shape[1], max_context, float(softmax_scale), _ptr(out),
-                                    ws.ptr(), ws.nbytes, _stream(q.device)))
+                                    bs, nb, table_blocks, max_context, float(softmax_scale), _ptr(out), ws.ptr(),
+                                    ws.nbytes, _stream(q.device)))
     return out

@@ -732,42 +732,51 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
   } else {
     // ------------------------------------------------------------ softmax
     regs_up<kCaRegsSoftmax>();
+    // A row's q, its output and its partial results are whole lines of memory:
+    // the warp moves them a row or more at a time, D / 8 lanes of 16 bytes a row.
+    constexpr int CH = D / 8, RPI = 32 / CH;
+    const int in_row = lane % CH;
     // q as f16 (a power-of-two scale a row brings its largest value to [1, 2):
     // exact, but for values 2^-24 of the largest and below)
-    float rowfac;
+    uint32_t my_ex = 1u;
     {
-      uint4 w[D / 8];
-      uint32_t amax = 0;
-      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(k.first_q + tok) * p.ldq +
-                                                         (int64_t)(kvh * p.G + head) * D);
-      #pragma unroll
-      for (int c = 0; c < D / 8; ++c) w[c] = has_row ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-      tmem_base = all_set();
-      #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+      const int64_t at = has_row ? (int64_t)(k.first_q + tok) * p.ldq + (int64_t)(kvh * p.G + head) * D : -1;
+      const uint32_t qs = smem_u32(sm + S::Q) + (two ? stream : 0) * S::kOperand;
+      #pragma unroll 1
+      for (int g = 0; g < 2; ++g) {   // half of the warp's rows
+        uint4 w[16 / RPI];
         #pragma unroll
-        for (int i = 0; i < 4; ++i) amax = max(amax, max((v[i] << 16) & 0x7FFFFFFFu, v[i] & 0x7FFF0000u));
-      }
-      // 2^e, e the exponent of the largest magnitude, kept where 2^-e is a normal number too
-      const uint32_t ex = min(max(amax >> 23, 1u), 253u);
-      const float up = __uint_as_float((254u - ex) << 23);
-      rowfac = __uint_as_float(ex << 23) * p.scale_log2;
-      if (two || stream == 0) {
-        uint8_t *qs = sm + S::Q + (two ? stream : 0) * S::kOperand;
-        #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-          uint32_t h[4];
-          #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            h[i] = f16_pair(__uint_as_float(v[i] << 16) * up, __uint_as_float(v[i] & 0xFFFF0000u) * up);
-          *reinterpret_cast<uint4 *>(qs + piece_off(lrow, c)) = make_uint4(h[0], h[1], h[2], h[3]);
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const int64_t from = __shfl_sync(0xffffffffu, at, 16 * g + i * RPI + lane / CH);
+          w[i] = from >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.q + from) + in_row) : make_uint4(0u, 0u, 0u, 0u);
         }
-        fence_async_shared();
-        mbar_arrive(q_full);
+        #pragma unroll
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          uint32_t amax = 0;
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) amax = max(amax, max((v[e] << 16) & 0x7FFFFFFFu, v[e] & 0x7FFF0000u));
+          #pragma unroll
+          for (int o = CH / 2; o >= 1; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // 2^e, e the exponent of the largest magnitude, kept where 2^-e is a normal number too
+          const uint32_t ex = min(max(amax >> 23, 1u), 253u);
+          const float up = __uint_as_float((254u - ex) << 23);
+          const uint32_t rows_ex = __shfl_sync(0xffffffffu, ex, (lane % RPI) * CH);
+          if (lane / RPI == 16 / RPI * g + i) my_ex = rows_ex;
+          if (two || stream == 0) {
+            uint32_t h[4];
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+              h[e] = f16_pair(__uint_as_float(v[e] << 16) * up, __uint_as_float(v[e] & 0xFFFF0000u) * up);
+            sts128(qs + piece_off((warp & 3) * 32 + 16 * g + i * RPI + lane / CH, in_row), h[0], h[1], h[2], h[3]);
+          }
+        }
       }
+      if (two || stream == 0) fence_async_shared();
+      tmem_base = all_set();
+      if (two || stream == 0) mbar_arrive(q_full);
     }
+    const float rowfac = __uint_as_float(my_ex << 23) * p.scale_log2;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem_base + lane_addr + stream * 128;        // S, then P'
     const uint32_t to = tmem_base + lane_addr + 256 + stream * D;    // O
@@ -1001,31 +1010,62 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         p.part_ml[part * 2] = l == 0.0f ? -INFINITY : r;
         p.part_ml[part * 2 + 1] = l;
       }
-      #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t x[32];
+      // Through this warp's part of the q area, whose products are done: 32 rows of D * 2 bytes.
+      const uint32_t area = smem_u32(sm + S::Q) + (two ? stream : 0) * S::kOperand + (warp & 3) * (32 * D * 2);
+      auto place = [&](int row, int c) { return area + row * (D * 2) + ((c ^ (row & (CH - 1))) << 4); };
+      // 32 of this row's values of O, as floats
+      auto values = [&](int col, uint32_t (&v)[32]) {
         __syncwarp();
-        tmem_ld_32x32b_x32(to + 32 * c, x);   // stale where no product was issued: f0 is 0 there
+        tmem_ld_32x32b_x32(to + col, v);   // stale where no product was issued: f0 is 0 there
         tmem_wait_ld();
-        float o[32];
+        arrived32(v);
         #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          o[i] = f0 == 0.0f ? 0.0f : __uint_as_float(x[i]) * f0;
-          if (f1 != 0.0f) o[i] = fmaf(joined[(32 * c + i) * kCaRows + lrow], f1, o[i]);
-        }
-        if (has_row && p.splits > 1) {
-          float4 *dst = reinterpret_cast<float4 *>(p.part_acc + part * D + 32 * c);
+        for (int i = 0; i < 32; ++i) v[i] = f0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(v[i]) * f0);
+        if (f1 != 0.0f) {
           #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        } else if (has_row) {
-          uint4 *dst = reinterpret_cast<uint4 *>(p.out + oh * D + 32 * c);
-          #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(bf16_pair(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                bf16_pair(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                bf16_pair(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                bf16_pair(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+          for (int i = 0; i < 32; ++i)
+            v[i] = __float_as_uint(fmaf(joined[(col + i) * kCaRows + lrow], f1, __uint_as_float(v[i])));
         }
+      };
+      // the area's rows, each to a place of its own
+      auto flush = [&](uint8_t *base, int64_t row_at, int64_t row_bytes_out) {
+        __syncwarp();
+        #pragma unroll 4
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int row = i * RPI + lane / CH;
+          const int64_t to_row = __shfl_sync(0xffffffffu, row_at, row);
+          const uint4 v = lds128(place(row, in_row));
+          if (to_row >= 0) *reinterpret_cast<uint4 *>(base + to_row * row_bytes_out + in_row * 16) = v;
+        }
+        __syncwarp();
+      };
+      if (p.splits > 1) {
+        #pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          #pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t v[32];
+            values(g * (D / 2) + 32 * c, v);
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) sts128(place(lane, 8 * c + i), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+          flush(reinterpret_cast<uint8_t *>(p.part_acc + g * (D / 2)), has_row ? part : -1, D * 4);
+        }
+      } else {
+        #pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          values(32 * c, v);
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[4];
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = bf16_pair(__uint_as_float(v[8 * i + 2 * e]) * inv, __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
+            sts128(place(lane, 4 * c + i), o[0], o[1], o[2], o[3]);
+          }
+        }
+        flush(reinterpret_cast<uint8_t *>(p.out), has_row ? oh : -1, D * 2);
       }
     }
   }
