@@ -91,11 +91,12 @@ int map_cache_selftest();
 // while the previous kernel in the stream finishes, and waits for it with
 // griddepcontrol.wait before touching global memory.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int block, cudaStream_t st, Args... args) {
+inline cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem, cudaStream_t st,
+                                   Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -103,6 +104,11 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int block, cu
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int block, cudaStream_t st, Args... args) {
+  return launch_pdl_smem(kernel, grid, block, 0, st, args...);
 }
 
 // Residual add and norms (norm.cu).  Pitches are in elements (multiples of

@@ -138,6 +138,91 @@ __device__ __forceinline__ uint64_t pack2(float a) {
   return r;
 }
 
+// Two fp32 values in a register pair: each operation rounds as the scalar one.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ float2 halves(uint64_t a) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(a));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+
+__device__ __forceinline__ uint64_t join2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(__float_as_uint(lo)), "r"(__float_as_uint(hi)));
+  return r;
+}
+
+// Eight bf16 -> four pairs of fp32, and back with one rounding.
+__device__ __forceinline__ void unpack8(const uint4 v, uint64_t (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = join2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
+  uint32_t w[4];
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = halves(f[i]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+    w[i] = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The scale of fp32 values whose largest magnitude is amax: amax / 448; 1 and
+// zero codes where that is 0 (all zero, or below the smallest float times 448).
+__device__ __forceinline__ GroupScale group_scale_f32(float amax) {
+  GroupScale g;
+  g.s = __fdiv_rn(amax, 448.0f);
+  g.mode = g.s >= kFastPathMinScale && g.s < __uint_as_float(0x7F800000u) ? kFast : kSlow;
+  if (g.s == 0.0f) {
+    g.s = 1.0f;
+    g.mode = kZeroGroup;
+  }
+  g.r = __frcp_rn(g.s);
+  return g;
+}
+
+// The codes of eight values given as their negations.
+__device__ __forceinline__ uint2 quant8_negated(const uint64_t (&nx)[4], const GroupScale &g) {
+  if (g.mode == kZeroGroup) return make_uint2(0u, 0u);
+  uint32_t c[4];
+  if (g.mode == kFast) {
+    const uint64_t s2 = pack2(g.s), nr2 = pack2(-g.r);
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = halves(nx[i]);
+      c[i] = quant_nx2_fast(__float_as_uint(v.x), __float_as_uint(v.y), s2, nr2);
+    }
+  } else {
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = halves(nx[i]);
+      const float2 q = make_float2(quotient(-v.x, g), quotient(-v.y, g));
+      c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+    }
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
 // Quantises n vectors src[j0], src[j0 + step], ... of one group into
 // dst[j] (8 codes each), choosing the arithmetic once for the whole run.
 template <typename Src>
