@@ -103,7 +103,7 @@ __device__ __forceinline__ void add_block(const NormArgs &p, const uint4 yv, con
   }
   const uint64_t a2 = pack2(p.a);
   #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = add2(h[i], mul2(a2, u[i]));
+  for (int i = 0; i < 4; ++i) h[i] = fma2(a2, u[i], h[i]);
 }
 
 // h -> z = h * w_pre, and what the row's sums take of it.

@@ -40,64 +40,35 @@ struct RopeArgs {
   float *ks, *vs;
 };
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&b);
-}
-
-// Codes of 8 values whose vector (L lanes) has the scale of its largest
-// magnitude; every lane of the warp takes part.
-template <int L>
-__device__ __forceinline__ uint2 quantise_vector(const float (&x)[8], float &scale) {
-  float amax = 0.0f;
-  #pragma unroll
-  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
-  #pragma unroll
-  for (int o = L / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  scale = __fdiv_rn(amax, 448.0f);
-  uint32_t c[4];
-  // an all-zero vector, or one whose scale underflows: scale 1, codes 0
-  const bool none = scale == 0.0f;
-  if (none) scale = 1.0f;
-  #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = make_float2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
-    c[i] = none ? 0u : (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-  }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-}
-
 template <int D, int N, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs p) {
   constexpr int L = D / 8;                    // lanes a head
   constexpr int kGroups = kRopeThreads / L;   // groups of lanes a CTA
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t t = blockIdx.x;
   const int lane = threadIdx.x % L, e0 = lane * 8;
-  const int heads = p.Hq + 2 * p.Hkv;
-  // this group's heads: h0, h0 + kGroups, ... (neighbouring groups read neighbouring heads)
-  const int h0 = blockIdx.y * (kGroups * N) + threadIdx.x / L;
-  const int64_t pos = p.positions[t], slot = p.slots[t];
-  if (pos < 0 || pos >= p.max_position) return;   // the whole CTA: one token
-  const bool keep = slot >= 0 && slot < p.num_slots;
+  const int heads = p.Hq + 2 * p.Hkv, per_token = (heads + N - 1) / N;   // groups of lanes a token
+  const uint32_t group = blockIdx.x * kGroups + threadIdx.x / L;
+  const int64_t t = group / (uint32_t)per_token;
+  // this group's heads: h0, h0 + per_token, ... (neighbouring groups read neighbouring heads)
+  const int h0 = (int)(group - (uint32_t)t * per_token);
+  const bool token = t < p.T;
+  const int64_t pos = token ? p.positions[t] : -1, slot = token ? p.slots[t] : -1;
+  const bool active = pos >= 0 && pos < p.max_position, keep = slot >= 0 && slot < p.num_slots;
   uint4 raw[N];
   #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int h = h0 + i * kGroups;
+    const int h = h0 + i * per_token;
+    const bool is_q = h < p.Hq, is_k = h < p.Hq + p.Hkv;
+    const uint4 *from = is_q ? p.q + t * p.ldq : is_k ? p.k + t * p.ldk : p.v + t * p.ldv;
     raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (h < p.Hq)
-      raw[i] = ld_stream(p.q + t * p.ldq + (int64_t)h * L + lane);
-    else if (h < p.Hq + p.Hkv)
-      raw[i] = ld_stream(p.k + t * p.ldk + (int64_t)(h - p.Hq) * L + lane);
-    else if (h < heads)
-      raw[i] = ld_stream(p.v + t * p.ldv + (int64_t)(h - p.Hq - p.Hkv) * L + lane);
+    if (active && h < heads) raw[i] = ld_stream(from + (int64_t)(h - (is_q ? 0 : is_k ? p.Hq : p.Hq + p.Hkv)) * L + lane);
   }
   // the angles of this lane's pairs: 8 (one half of each pair is here), or 4
-  // when interleaved (both halves are)
+  // when interleaved (both halves are); cosine 1 and sine 0 where nothing turns
   constexpr int A = INTERLEAVED ? 4 : 8;
   const int half = p.rot / 2;
-  const bool turns = e0 < p.rot;
+  const bool turns = active && e0 < p.rot;
   const bool upper = !INTERLEAVED && e0 >= half;   // holds the pairs' second halves
   float c[A], s[A];
   if (turns) {
@@ -111,55 +82,69 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
       s[4 * i] = b.x; s[4 * i + 1] = b.y; s[4 * i + 2] = b.z; s[4 * i + 3] = b.w;
     }
   }
+  // first halves take a c - b s, second ones b c + a s: a - is a negated sine
+  uint64_t c2[4], s2[4];
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (INTERLEAVED) {
+      c2[i] = pack2(c[i % A]);
+      s2[i] = join2(-s[i % A], s[i % A]);
+    } else {
+      c2[i] = join2(c[(2 * i) % A], c[(2 * i + 1) % A]);
+      s2[i] = upper ? join2(s[(2 * i) % A], s[(2 * i + 1) % A]) : join2(-s[(2 * i) % A], -s[(2 * i + 1) % A]);
+    }
+  }
   // the lane that holds the other halves of this lane's pairs (itself where nothing turns)
-  const int other = INTERLEAVED || !turns ? threadIdx.x & 31
-                                          : (threadIdx.x & 31) + (upper ? -(half / 8) : half / 8);
+  const int self = threadIdx.x & 31;
+  const int other = INTERLEAVED || e0 >= p.rot ? self : self + (upper ? -(half / 8) : half / 8);
   #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int h = h0 + i * kGroups;
-    float x[8];
-    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-    #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = __uint_as_float(w[j] << 16);
-      x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-    uint32_t o[4] = {0u, 0u, 0u, 0u};
+    const int h = h0 + i * per_token;
+    uint4 mate = raw[i];
     if (!INTERLEAVED) {
-      #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = __shfl_sync(0xffffffffu, w[j], other);
+      mate.x = __shfl_sync(0xffffffffu, raw[i].x, other);
+      mate.y = __shfl_sync(0xffffffffu, raw[i].y, other);
+      mate.z = __shfl_sync(0xffffffffu, raw[i].z, other);
+      mate.w = __shfl_sync(0xffffffffu, raw[i].w, other);
     }
+    uint64_t x[4];
+    unpack8(raw[i], x);
     if (turns && h < p.Hq + p.Hkv) {
-      if (INTERLEAVED) {
-        #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float a = x[2 * j], b = x[2 * j + 1];
-          x[2 * j] = __fsub_rn(__fmul_rn(a, c[j]), __fmul_rn(b, s[j]));
-          x[2 * j + 1] = __fadd_rn(__fmul_rn(b, c[j]), __fmul_rn(a, s[j]));
+      uint64_t y[4];
+      unpack8(mate, y);
+      #pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (INTERLEAVED) {
+          const float2 v = halves(x[e]);
+          y[e] = join2(v.y, v.x);
         }
-      } else {
-        #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = e % 2 == 0 ? __uint_as_float(o[e / 2] << 16) : __uint_as_float(o[e / 2] & 0xFFFF0000u);
-          const float own = __fmul_rn(x[e], c[e % A]), mix = __fmul_rn(y, s[e % A]);
-          x[e] = upper ? __fadd_rn(own, mix) : __fsub_rn(own, mix);
-        }
+        // scalar sums: the compiler makes one fused operation of a packed product and a packed sum
+        const float2 own = halves(mul2(x[e], c2[e])), mix = halves(mul2(y[e], s2[e]));
+        x[e] = join2(__fadd_rn(own.x, mix.x), __fadd_rn(own.y, mix.y));
       }
     }
     // the groups of a warp may hold heads of different kinds, and their
     // shuffles are the warp's: decided for the warp as a whole
-    const bool stores_codes = h >= p.Hq && h < heads;
-    if (h < p.Hq)
-      p.q_out[t * p.ldo + (int64_t)h * L + lane] =
-          make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
-    if (__any_sync(0xffffffffu, stores_codes)) {
-      float scale;
-      const uint2 code = quantise_vector<L>(x, scale);
-      if (stores_codes && keep) {
+    const bool is_kv = active && h >= p.Hq && h < heads;
+    if (active && h < p.Hq) p.q_out[t * p.ldo + (int64_t)h * L + lane] = pack8(x);
+    if (__any_sync(0xffffffffu, is_kv)) {
+      float amax = 0.0f;
+      #pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = halves(x[e]);
+        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+      }
+      #pragma unroll
+      for (int o = L / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (is_kv && keep) {
+        const GroupScale g = group_scale_f32(amax);
+        const uint64_t minus = pack2(-1.0f);
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], minus);
         const bool is_v = h >= p.Hq + p.Hkv;
         const int64_t at = slot * p.Hkv + (h - p.Hq - (is_v ? p.Hkv : 0));
-        reinterpret_cast<uint2 *>((is_v ? p.vc : p.kc) + at * D)[lane] = code;
-        if (lane == 0) (is_v ? p.vs : p.ks)[at] = scale;
+        reinterpret_cast<uint2 *>((is_v ? p.vc : p.kc) + at * D)[lane] = quant8_negated(x, g);
+        if (lane == 0) (is_v ? p.vs : p.ks)[at] = g.s;
       }
     }
   }
@@ -167,8 +152,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
 
 template <int D, int N>
 cudaError_t launch_n(const RopeArgs &p, bool interleaved, cudaStream_t st) {
-  const int per_cta = kRopeThreads / (D / 8) * N;
-  const dim3 grid(p.T, (p.Hq + 2 * p.Hkv + per_cta - 1) / per_cta);
+  const int64_t groups = (int64_t)p.T * ((p.Hq + 2 * p.Hkv + N - 1) / N);
+  constexpr int kGroups = kRopeThreads / (D / 8);
+  // groups are counted in 32 bits: more are more than the memory of a GPU holds
+  if (groups > 0xFFFFFF00ll) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)((groups + kGroups - 1) / kGroups));
   return interleaved ? launch_pdl(rope_append_kernel<D, N, true>, grid, kRopeThreads, st, p)
                      : launch_pdl(rope_append_kernel<D, N, false>, grid, kRopeThreads, st, p);
 }
