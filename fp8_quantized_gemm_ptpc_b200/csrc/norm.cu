@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(V <= 2 ? 1024 : 512) residual_norm_kernel(cons
 }
 
 // Rows enough for several a CTA: CTAs that stay, with what is the same for
-// every row kept in shared memory as fp32, F = a * w_post * (the channels'
-// gate) and w_pre.  A vector of both takes 4 loads in place of 3, and 36
+// every row kept in shared memory as fp32, F = w_post * (the channels'
+// gate) * a and w_pre.  A vector of both takes 4 loads in place of 3, and 36
 // instructions less.  The next row's loads are issued as soon as this one's
 // registers are free, ahead of its second reduction.
 constexpr int kStayV = 4;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(512) residual_norm_stay_kernel(const NormArgs 
   for (int j = threadIdx.x; j < p.nvec; j += blockDim.x) {
     uint64_t f[4], w[4];
     #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = pack2(p.a);
+    for (int i = 0; i < 4; ++i) f[i] = pack2(1.0f);
     if (p.wpost != nullptr) {
       unpack8(__ldg(p.wpost + j), w);
       #pragma unroll
@@ -229,6 +229,8 @@ __global__ void __launch_bounds__(512) residual_norm_stay_kernel(const NormArgs 
       #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w[i]);
     }
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], pack2(p.a));
     ulonglong2 *to = reinterpret_cast<ulonglong2 *>(factors) + j;
     to[0] = make_ulonglong2(f[0], f[1]);
     to[p.nvec] = make_ulonglong2(f[2], f[3]);

@@ -126,6 +126,17 @@ def test_strides_in_place_and_first_norm(ptpc, T, C, quant):
     check(ptpc, T, C, quant, first=True)
 
 
+@pytest.mark.parametrize("T,C,post,gate,a,more", [
+    (1200, 8192, True, "channel", 0.7, {}), (2369, 4096, False, None, 1.0, dict(inplace=True)),
+    (1185, 7200, True, "token", 0.5, dict(pad=16)), (600, 16384, True, None, -1.5, dict(inplace=True, pad=8)),
+    (9500, 1024, False, "token", 1.0, {}), (2400, 4080, False, "channel", 0.25, dict(zero_rows=(0, 1111, 2399))),
+    (2401, 3600, True, "token", 1.0, {}), (1184, 8208, False, None, 1.0, dict(first=True)),
+    (1187, 8192, False, None, 1.0, dict(first=True, tiny_rows=(0, 1186)))])
+@pytest.mark.parametrize("quant", [True, False])
+def test_several_rows_a_cta(ptpc, T, C, post, gate, a, more, quant):
+    check(ptpc, T, C, quant, post=post, gate=gate, a=a, **more)
+
+
 @pytest.mark.parametrize("quant", [True, False])
 def test_zero_and_tiny_rows(ptpc, quant):
     """Rows of zeros (the norm's eps alone: x = 0, scale 1, codes 0) and rows so
