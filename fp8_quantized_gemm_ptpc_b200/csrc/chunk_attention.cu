@@ -136,6 +136,11 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -370,6 +375,14 @@ __device__ __forceinline__ bool find_work(const ChunkArgs &p, int w, Work &k) {
   }
   return false;
 }
+
+// 16 bytes from memory into shared memory, asynchronously; zeros where `in` is
+// false (nothing is read then).
+__device__ __forceinline__ void copy16_or_zero(uint32_t to, const void *from, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <int D>
 __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkArgs p) {
@@ -733,50 +746,65 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     // ------------------------------------------------------------ softmax
     regs_up<kCaRegsSoftmax>();
     // A row's q, its output and its partial results are whole lines of memory:
-    // the warp moves them a row or more at a time, D / 8 lanes of 16 bytes a row.
+    // the warp moves them a row or more at a time, D / 8 lanes of 16 bytes a
+    // row, through its rows' place in shared memory.  What runs once a CTA is
+    // kept small, in loops: it comes from beyond the instruction cache.
     constexpr int CH = D / 8, RPI = 32 / CH;
     const int in_row = lane % CH;
-    // q as f16 (a power-of-two scale a row brings its largest value to [1, 2):
-    // exact, but for values 2^-24 of the largest and below)
-    uint32_t my_ex = 1u;
+    const uint32_t qs = smem_u32(sm + S::Q) + stream * S::kOperand;
     {
-      const int64_t at = has_row ? (int64_t)(k.first_q + tok) * p.ldq + (int64_t)(kvh * p.G + head) * D : -1;
-      const uint32_t qs = smem_u32(sm + S::Q) + (two ? stream : 0) * S::kOperand;
-      #pragma unroll 1
-      for (int g = 0; g < 2; ++g) {   // half of the warp's rows
-        uint4 w[16 / RPI];
-        #pragma unroll
-        for (int i = 0; i < 16 / RPI; ++i) {
-          const int64_t from = __shfl_sync(0xffffffffu, at, 16 * g + i * RPI + lane / CH);
-          w[i] = from >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.q + from) + in_row) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        #pragma unroll
-        for (int i = 0; i < 16 / RPI; ++i) {
-          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          uint32_t amax = 0;
-          #pragma unroll
-          for (int e = 0; e < 4; ++e) amax = max(amax, max((v[e] << 16) & 0x7FFFFFFFu, v[e] & 0x7FFF0000u));
-          #pragma unroll
-          for (int o = CH / 2; o >= 1; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          // 2^e, e the exponent of the largest magnitude, kept where 2^-e is a normal number too
-          const uint32_t ex = min(max(amax >> 23, 1u), 253u);
-          const float up = __uint_as_float((254u - ex) << 23);
-          const uint32_t rows_ex = __shfl_sync(0xffffffffu, ex, (lane % RPI) * CH);
-          if (lane / RPI == 16 / RPI * g + i) my_ex = rows_ex;
-          if (two || stream == 0) {
-            uint32_t h[4];
-            #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              h[e] = f16_pair(__uint_as_float(v[e] << 16) * up, __uint_as_float(v[e] & 0xFFFF0000u) * up);
-            sts128(qs + piece_off((warp & 3) * 32 + 16 * g + i * RPI + lane / CH, in_row), h[0], h[1], h[2], h[3]);
-          }
-        }
+      const int64_t from = has_row ? (int64_t)(k.first_q + tok) * p.ldq + (int64_t)(kvh * p.G + head) * D : -1;
+      #pragma unroll 2
+      for (int i = 0; i < 32; i += RPI) {
+        const int64_t at = __shfl_sync(0xffffffffu, from, i + lane / CH);
+        copy16_or_zero(qs + piece_off((warp & 3) * 32 + i + lane / CH, in_row), p.q + max(at, (int64_t)0) + in_row * 8, at >= 0);
       }
-      if (two || stream == 0) fence_async_shared();
-      tmem_base = all_set();
-      if (two || stream == 0) mbar_arrive(q_full);
     }
-    const float rowfac = __uint_as_float(my_ex << 23) * p.scale_log2;
+    tmem_base = all_set();
+    copies_done();
+    __syncwarp();
+    // q as f16 (a power-of-two scale a row brings its largest value to [1, 2):
+    // exact, but for values 2^-24 of the largest and below), in place
+    constexpr int kAtOnce = 4;
+    uint32_t tops = 0;   // the largest magnitudes of the row's even and odd values, as bits
+    uint4 qv[kAtOnce];
+    auto take_q = [&](int c) {
+      #pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) qv[i] = lds128(qs + piece_off(lrow, c + i));
+    };
+    #pragma unroll 1
+    for (int c = 0; c < CH; c += kAtOnce) {
+      take_q(c);
+      #pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) tops = __vmaxu2(tops, w[e] & 0x7FFF7FFFu);
+      }
+    }
+    // 2^e, e the exponent of the largest magnitude, kept where 2^-e is a normal number too
+    const uint32_t ex = min(max(max(tops >> 16, tops & 0xFFFFu) >> 7, 1u), 253u);
+    const float up = __uint_as_float((254u - ex) << 23);
+    const uint64_t up2 = pack_f32x2(up, up);
+    #pragma unroll 1
+    for (int c = 0; c < CH; c += kAtOnce) {
+      take_q(c);
+      #pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+        uint32_t h[4];
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack_f32x2(mul_f32x2(
+              pack_f32x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)), up2));
+          h[e] = f16_pair(f.x, f.y);
+        }
+        sts128(qs + piece_off(lrow, c + i), h[0], h[1], h[2], h[3]);
+      }
+    }
+    fence_async_shared();
+    if (two || stream == 0) mbar_arrive(q_full);
+    const float rowfac = __uint_as_float(ex << 23) * p.scale_log2;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem_base + lane_addr + stream * 128;        // S, then P'
     const uint32_t to = tmem_base + lane_addr + 256 + stream * D;    // O
@@ -996,7 +1024,8 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       for (int j = max(0, k.tiles - 3); j < k.tiles; ++j) {
         if ((k.t0 + j + 1) * kCaTile <= all_see) continue;
         const TileMeta &tm = meta[j % kCaMeta];
-        #pragma unroll
+        if ((tm.nan[0] | tm.nan[1] | tm.nan[2] | tm.nan[3]) == 0) continue;
+        #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           const int n = sees - ((k.t0 + j) * kCaTile + 32 * c);
           const uint32_t causal = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
@@ -1010,62 +1039,59 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         p.part_ml[part * 2] = l == 0.0f ? -INFINITY : r;
         p.part_ml[part * 2 + 1] = l;
       }
-      // Through this warp's part of the q area, whose products are done: 32 rows of D * 2 bytes.
-      const uint32_t area = smem_u32(sm + S::Q) + (two ? stream : 0) * S::kOperand + (warp & 3) * (32 * D * 2);
+      // Through this warp's part of the q area, whose products are done: 32
+      // rows of D * 2 bytes, the outputs or half of the partial sums.
+      const uint32_t area = qs + (warp & 3) * (32 * D * 2);
       auto place = [&](int row, int c) { return area + row * (D * 2) + ((c ^ (row & (CH - 1))) << 4); };
-      // 32 of this row's values of O, as floats
-      auto values = [&](int col, uint32_t (&v)[32]) {
+      const int64_t row_at = !has_row ? -1 : p.splits > 1 ? part * (D * 4) : oh * (D * 2);
+      uint8_t *base = p.splits > 1 ? reinterpret_cast<uint8_t *>(p.part_acc) : reinterpret_cast<uint8_t *>(p.out);
+      const float f = p.splits > 1 ? f0 : f0 * inv, fj = p.splits > 1 ? f1 : f1 * inv;
+      const uint64_t ff = pack_f32x2(f, f);
+      #pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
         __syncwarp();
-        tmem_ld_32x32b_x32(to + col, v);   // stale where no product was issued: f0 is 0 there
+        tmem_ld_32x32b_x32(to + 32 * c, v);   // stale where no product was issued: f0 is 0 there
         tmem_wait_ld();
         arrived32(v);
         #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = f0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(v[i]) * f0);
+        for (int i = 0; i < 32; i += 2) {
+          const float2 w = unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), ff));
+          v[i] = __float_as_uint(w.x);
+          v[i + 1] = __float_as_uint(w.y);
+        }
+        if (f0 == 0.0f) {
+          #pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
         if (f1 != 0.0f) {
           #pragma unroll
           for (int i = 0; i < 32; ++i)
-            v[i] = __float_as_uint(fmaf(joined[(col + i) * kCaRows + lrow], f1, __uint_as_float(v[i])));
+            v[i] = __float_as_uint(fmaf(joined[(32 * c + i) * kCaRows + lrow], fj, __uint_as_float(v[i])));
         }
-      };
-      // the area's rows, each to a place of its own
-      auto flush = [&](uint8_t *base, int64_t row_at, int64_t row_bytes_out) {
-        __syncwarp();
-        #pragma unroll 4
-        for (int i = 0; i < 32 / RPI; ++i) {
-          const int row = i * RPI + lane / CH;
-          const int64_t to_row = __shfl_sync(0xffffffffu, row_at, row);
-          const uint4 v = lds128(place(row, in_row));
-          if (to_row >= 0) *reinterpret_cast<uint4 *>(base + to_row * row_bytes_out + in_row * 16) = v;
-        }
-        __syncwarp();
-      };
-      if (p.splits > 1) {
-        #pragma unroll 1
-        for (int g = 0; g < 2; ++g) {
-          #pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {
-            uint32_t v[32];
-            values(g * (D / 2) + 32 * c, v);
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) sts128(place(lane, 8 * c + i), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-          flush(reinterpret_cast<uint8_t *>(p.part_acc + g * (D / 2)), has_row ? part : -1, D * 4);
-        }
-      } else {
-        #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t v[32];
-          values(32 * c, v);
+        const bool halved = p.splits > 1;
+        if (halved) {
           #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[4];
-            #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[e] = bf16_pair(__uint_as_float(v[8 * i + 2 * e]) * inv, __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
-            sts128(place(lane, 4 * c + i), o[0], o[1], o[2], o[3]);
-          }
+          for (int i = 0; i < 8; ++i)
+            sts128(place(lane, (8 * c + i) & (CH - 1)), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+          #pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          #pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sts128(place(lane, 4 * c + i), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
-        flush(reinterpret_cast<uint8_t *>(p.out), has_row ? oh : -1, D * 2);
+        if (c != D / 32 - 1 && !(halved && c == D / 64 - 1)) continue;
+        // the area is full: its rows, each to a place of its own
+        __syncwarp();
+        uint8_t *to_half = base + (halved && c == D / 32 - 1 ? D * 2 : 0) + in_row * 16;
+        #pragma unroll 4
+        for (int i = 0; i < 32; i += RPI) {
+          const int64_t at = __shfl_sync(0xffffffffu, row_at, i + lane / CH);
+          const uint4 w = lds128(place(i + lane / CH, in_row));
+          if (at >= 0) *reinterpret_cast<uint4 *>(to_half + at) = w;
+        }
+        __syncwarp();
       }
     }
   }
