@@ -100,6 +100,10 @@ int run_gemm(const uint8_t *Xq, const float *xs, const uint8_t *Wq_t, const floa
   p.f32_out = f32_out;
   p.status = reinterpret_cast<uint32_t *>(wsp);
   p.pdl = pdl;
+  if (!pdl && !f32_out) {   // a dependent launch has its counters zeroed ahead of the kernel it follows
+    const int s = cuda_status(ptpc::zero_gemm_counters(p.T, p.Ci, p.Co, wsp, ws_bytes, st));
+    if (s != PTPC_OK) return s;
+  }
   return cuda_status(ptpc::launch_scaled_gemm(p, st));
 }
 
@@ -283,6 +287,7 @@ int ptpc_linear(const void *X, int64_t ldx, const uint8_t *Wq_t, const float *w_
   uint8_t *Xq = wsp + gws;
   float *xs = reinterpret_cast<float *>(wsp + gws + round_up((size_t)T * (size_t)Ci));
   cudaStream_t st = (cudaStream_t)stream;
+  if ((s = cuda_status(ptpc::zero_gemm_counters((int)T, (int)Ci, (int)Co, wsp, gws, st))) != PTPC_OK) return s;
   if ((s = cuda_status(ptpc::launch_quant_act(X, (int)T, (int)Ci, ldx, Xq, xs, st))) != PTPC_OK) return s;
   return run_gemm(Xq, xs, Wq_t, w_scale, T, Ci, Co, out, false, wsp, gws, true, st);
 }
@@ -347,6 +352,7 @@ int ptpc_linear_fmt(const void *X, int64_t ldx, const uint8_t *Wq, const float *
   uint8_t *Xq = wsp + gws;
   float *xs = reinterpret_cast<float *>(wsp + gws + round_up((size_t)T * (size_t)Ci));
   cudaStream_t st = (cudaStream_t)stream;
+  if ((s = cuda_status(ptpc::zero_gemm_counters((int)T, (int)Ci, (int)Co, wsp, gws, st))) != PTPC_OK) return s;
   if ((s = cuda_status(ptpc::launch_quant_act(X, (int)T, (int)Ci, ldx, Xq, xs, st))) != PTPC_OK) return s;
   return run_gemm(Xq, xs, Wq, w_scale, T, Ci, Co, out, false, wsp, gws, true, st, fmt);
 }

@@ -586,8 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // itself in, waits (bounded) until the tile's 2 * tail_split CTAs have all
 // stored theirs, and then finishes 1 / (2 * tail_split) of the tile: the
 // partials added in split order (a fixed order: deterministic), the two
-// scales applied, bf16 stored.  The last CTA to finish zeroes the tile's
-// counters for the next call.
+// scales applied, bf16 stored.  The counters are zeroed before each launch
+// (zero_gemm_counters): other entry points keep data in the same bytes.
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -1740,6 +1740,12 @@ size_t gemm_workspace_bytes(int T, int Ci, int Co) {
   const int num_kb = (Ci + BK - 1) / BK;
   if (T <= kDecodeWholeMaxT || num_kb < 2 * kMinTailKb) return kGemmStatusBytes;
   return kGemmStatusBytes + tail_workspace(1, kMaxTailPairs, 256);
+}
+
+cudaError_t zero_gemm_counters(int T, int Ci, int Co, uint8_t *ws, size_t ws_bytes, cudaStream_t st) {
+  if (ws_bytes <= kGemmStatusBytes + kTailCountBytes) return cudaSuccess;   // no room for partial sums: no split tail
+  if (make_plan(T, Ci, Co, ws_bytes).tail_tiles == 0) return cudaSuccess;
+  return cudaMemsetAsync(ws + kGemmStatusBytes, 0, kTailCountBytes, st);
 }
 
 cudaError_t launch_scaled_gemm(const GemmProblem &pr, cudaStream_t st) {

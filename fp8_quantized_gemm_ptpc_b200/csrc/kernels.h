@@ -58,6 +58,11 @@ struct GemmProblem {
 
 cudaError_t launch_scaled_gemm(const GemmProblem &p, cudaStream_t st);
 
+// Zeroes the split tail's counters where the shape's plan has one; enqueued
+// ahead of launch_scaled_gemm (of the kernel it depends on, with pdl).  The
+// workspace may have served another entry point since, whose data lay there.
+cudaError_t zero_gemm_counters(int T, int Ci, int Co, uint8_t *ws, size_t ws_bytes, cudaStream_t st);
+
 // CTAs per tile the decode kernel uses for a shape (1: whole tiles; larger:
 // K split over a cluster of that many CTAs).  For tests and reports.
 int gemm_ksplit(int T, int Ci, int Co);

@@ -40,8 +40,9 @@
  *   - Workspace: entry points that take (ws_dev, ws_bytes) need at least
  *     ptpc_workspace_size(op, T, Ci, Co) bytes, zero-filled before its first
  *     use.  Each successful call leaves the workspace's control words zero
- *     again, so a workspace is zero-filled only once.  Calls that share a
- *     workspace must not overlap on the GPU.
+ *     again, so a workspace is zero-filled only once.  Entry points may share
+ *     one, call behind call; calls that share a workspace must not overlap on
+ *     the GPU.
  *   - Inputs are assumed finite.  Non-finite inputs do not fault but give
  *     unspecified codes.  The GEMM epilogue multiplies in the order
  *     (acc * x_scale) * w_scale in fp32; outputs are specified where that
