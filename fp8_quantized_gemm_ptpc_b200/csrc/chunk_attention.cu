@@ -10,17 +10,17 @@
 //
 // Warps 8-11 (K) and 12-15 (V) read the codes (16 bytes a lane; any block size;
 // a tile ahead, in registers), turn them into f16 and lay them out in shared
-// memory for the MMAs.  The scales go in here, relative to a reference of each 32 positions
-// (a warp's rows):  K' = code * ks / kref,  V' = code * vs / vref, so that the
-// softmax has one factor for 32 columns instead of one a column.  kref is a
-// power of two at least the largest key scale; the product is formed as code *
-// hi + code * lo with the ratio split in two f16, so K' is rounded once.  vref
-// is 2^-6 of such a power for the value scales: V' reaches 448 * 64, near f16's largest
-// value, so that the ratio keeps f16's 11 bits down to 2^-20 of the largest
-// scale.  A key's error is 2^-12 of its value, spread over D products; a
-// value's at most 2^-11.
-// Warps 16 and 17 (a stream each) issue S = Q K'^T (kind::f16, q as f16 after a power-of-two scale a
-// row, exact) and O += P V' with P from tensor memory.
+// memory for the MMAs.  The scales go in here, relative to a reference of each
+// 32 positions (a warp's rows):  K' = code * ks / kref,  V' = code * vs / vref,
+// so that the softmax has one factor for 32 columns instead of one a column.
+// kref is a power of two at least the largest key scale; the product is formed
+// as code * hi + code * lo with the ratio split in two f16, so K' is rounded
+// once.  vref is 2^-6 of such a power for the value scales: V' reaches 448 *
+// 64, near f16's largest value, so that the ratio keeps f16's 11 bits down to
+// 2^-20 of the largest scale.  A key's error is 2^-12 of its value, spread over
+// D products; a value's at most 2^-11.
+// Warps 16 and 17 (a stream each) issue S = Q K'^T (kind::f16, q as f16 after a
+// power-of-two scale a row, exact) and O += P' V' with P' from tensor memory.
 // Warps 0-3 and 4-7 (a stream each, a thread a row) do the softmax in base 2.
 // With t = S * kref * qscale * log2 e, a weight is P' = 2^(t + log2 vref - r):
 // the reference r follows the largest t + log2 vref, so the f16 P' stays near
@@ -28,17 +28,32 @@
 // vref.  r moves (and O, in tensor memory, is rescaled) only when the weights
 // of 64 positions, taken with the r of before, sum to 2^15 or more, which also
 // keeps each below f16's largest value: the common case needs no maximum at
-// all.  A row's first r is the maximum of its first 64 positions.  P' overwrites
-// S in place.
+// all.  A row's first r is the maximum of its first 64 positions.  P'
+// overwrites S in place.
 // A tile goes through in halves of 64 positions, each with scores of its own in
-// tensor memory, so that a stream's products of one half run while its softmax
-// works on the other, and both streams' softmaxes never wait for theirs.  A CTA with 128
-// rows or fewer gives both streams the same rows and every other tile each,
-// and joins them at the end.
+// tensor memory: a stream's products of one half run while its softmax works on
+// the other.  A CTA with 128 rows or fewer gives both streams the same rows and
+// every other tile each, and joins them at the end.
 //
 // With few rows the context is split over CTAs whose partial results a second
 // kernel joins (plan_chunk).  Every wait is bounded; a timeout sets a bit in
 // the status word at the front of the workspace.
+//
+// What bounds it (B200, 64 + 8 heads of 128).  64 positions of both streams take
+// about 1,900 cycles of an SM, in which the products need 620 (the MMAs of 64
+// columns read shared memory for 49 cycles each, 16 columns of depth a time) and
+// the exponentials' unit is busy for 1,024; with the conversions the schedulers
+// issue in two cycles of three.  With 128 rows or fewer the conversions bound it:
+// 3,100 cycles for 128 positions.  A CTA's start and end cost about 17,000 cycles
+// (its places 1,200, the first codes and q 7,000, the first scores, its last
+// product and output 6,500, the next CTA's launch 2,500), which is why a context
+// is split only in parts of some tiles.  2048 tokens on 30,720 more: 1.96 ms, 0.66
+// of the measured bf16 rate; prompts of 300 to 4000 tokens 539 us, 0.48.
+// Measured and dropped: scores of 128 columns (the MMAs of both streams then
+// collide, and shared memory answers the converters late), one S buffer and two of
+// P' a stream, four softmax warpgroups of half a row, P' and the next scores'
+// loads in the other order, codes kept in shared memory, L2 prefetches two tiles
+// ahead (8% faster for single tokens, 2% slower for chunks).
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -1146,8 +1161,9 @@ struct ChunkPlan {
 };
 
 // Row tiles, and the CTAs that share a context.  A part costs its tiles and a
-// start and end worth kFixed tiles; the parts of the last wave leave SMs idle,
-// so the split with the least (waves x cost) is taken.
+// start and end worth kFixed tiles (3 to 6 measured alike); the parts of the last
+// wave leave SMs idle, so the split with the least (waves x cost) is taken.  One
+// sequence of 5 tokens on 4096 positions: 24.6 us.
 ChunkPlan plan_chunk(int64_t total_q, int64_t B, int Hkv, int G, int64_t max_q, int64_t max_context) {
   constexpr int64_t kFixed = 6;
   ChunkPlan c;
