@@ -39,21 +39,24 @@
 // kernel joins (plan_chunk).  Every wait is bounded; a timeout sets a bit in
 // the status word at the front of the workspace.
 //
-// What bounds it (B200, 64 + 8 heads of 128).  64 positions of both streams take
-// about 1,900 cycles of an SM, in which the products need 620 (the MMAs of 64
-// columns read shared memory for 49 cycles each, 16 columns of depth a time) and
-// the exponentials' unit is busy for 1,024; with the conversions the schedulers
-// issue in two cycles of three.  With 128 rows or fewer the conversions bound it:
-// 3,100 cycles for 128 positions.  A CTA's start and end cost about 17,000 cycles
-// (its places 1,200, the first codes and q 7,000, the first scores, its last
-// product and output 6,500, the next CTA's launch 2,500), which is why a context
-// is split only in parts of some tiles.  2048 tokens on 30,720 more: 1.96 ms, 0.66
-// of the measured bf16 rate; prompts of 300 to 4000 tokens 539 us, 0.48.
+// What bounds it (B200, heads of 128).  64 positions of both streams take about
+// 1,900 cycles of an SM, in which the products need 620 (the MMAs of 64 columns
+// read shared memory for 49 cycles each, 16 columns of depth a time) and the
+// exponentials' unit is busy for 1,024; the schedulers issue in 57% of the
+// cycles, the rest is latency.  With 128 rows or fewer the conversions bound it:
+// 3,100 cycles for 128 positions.  A CTA's start and end cost about 17,000
+// cycles (its places 1,200, the first codes and q 7,000, the first scores, its
+// last product and output 6,500, the next CTA's launch 2,500), which is why a
+// context is split only in parts of some tiles.  With 64 + 8 heads, 2048 tokens on
+// 30,720 more take 1.96 ms, 0.66 of the measured bf16 rate; with 32 + 8, eight
+// prompts of 300 to 4000 tokens 539 us, 0.48.
 // Measured and dropped: scores of 128 columns (the MMAs of both streams then
-// collide, and shared memory answers the converters late), one S buffer and two of
-// P' a stream, four softmax warpgroups of half a row, P' and the next scores'
-// loads in the other order, codes kept in shared memory, L2 prefetches two tiles
-// ahead (8% faster for single tokens, 2% slower for chunks).
+// collide, and shared memory answers the converters late), one S buffer and two
+// of P' a stream, four softmax warpgroups, the next scores' loads ahead of P'
+// (all slower); converter code apart for whole tiles (no gain); a polynomial for
+// one exponential in sixteen (3% faster, not kept for its special cases), for more
+// (slower); L2 prefetches two tiles ahead (8% faster for single tokens, 2% slower
+// for chunks).
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
