@@ -47,7 +47,7 @@
 // 3,100 cycles for 128 positions.  A CTA's start and end cost about 17,000
 // cycles (its places 1,200, the first codes and q 7,000, the first scores, its
 // last product and output 6,500, the next CTA's launch 2,500), which is why a
-// context is split only in parts of some tiles.  With 64 + 8 heads, 2048 tokens on
+// context is split only where SMs would idle.  With 64 + 8 heads, 2048 tokens on
 // 30,720 more take 1.96 ms, 0.66 of the measured bf16 rate; with 32 + 8, eight
 // prompts of 300 to 4000 tokens 539 us, 0.48.
 // Measured and dropped: scores of 128 columns (the MMAs of both streams then
@@ -1164,24 +1164,33 @@ struct ChunkPlan {
 };
 
 // Row tiles, and the CTAs that share a context.  A part costs its tiles and a
-// start and end worth kFixed tiles (3 to 6 measured alike); the parts of the last
-// wave leave SMs idle, so the split with the least (waves x cost) is taken.  One
-// sequence of 5 tokens on 4096 positions: 24.6 us.
+// start and end worth kFixed tiles, and the parts of the last wave leave SMs
+// idle: the split with the least (waves x cost) is taken, where a split also
+// pays for the second kernel and its partial results (kRowsATile rows a part
+// take it about a tile's time).  The launch has room for the most row tiles that
+// the bounds allow; the waves are counted for the middle between those and the
+// fewest.  Measured over 26 shapes (geometric means): 43.6 us, with kFixed 6,
+// parts of four tiles or more and the most row tiles 48.3; the middle alone took
+// 67 tokens on 57,435 positions and 64 on 41,014, 32 + 2 heads of 64, from 137 to
+// 121 us; the fewest would put a sequence of one row tile more into a second wave
+// (72 -> 92 us).  One sequence of 5 tokens on 4096 positions: 22.5 us.
 ChunkPlan plan_chunk(int64_t total_q, int64_t B, int Hkv, int G, int64_t max_q, int64_t max_context) {
-  constexpr int64_t kFixed = 6;
+  constexpr int64_t kFixed = 3, kRowsATile = 12000;
   ChunkPlan c;
   c.row_tiles = std::min(total_q * G / (2 * kCaRows) + B, B * ((max_q * G + 2 * kCaRows - 1) / (2 * kCaRows)));
   const int64_t tiles = std::max<int64_t>(1, (max_context + kCaTile - 1) / kCaTile);
-  const int64_t ctas = c.row_tiles * Hkv, sms = num_sms();
+  const int64_t sms = num_sms(), rows = total_q * G * Hkv;
+  const int64_t fewest = std::max(B, (total_q * G + 2 * kCaRows - 1) / (2 * kCaRows));
+  const int64_t ctas = std::max<int64_t>(1, (std::min(fewest, c.row_tiles) + c.row_tiles) / 2) * Hkv;
   int64_t best = -1;
   c.splits = 1;
   c.split_tiles = (int)tiles;
   for (int64_t s = 1; s <= kCaMaxSplits; ++s) {
     const int64_t each = (tiles + s - 1) / s;
-    if (s > 1 && (each < 4 || ctas * s > 8 * sms)) break;
+    if (s > 1 && (each < 2 || ctas * s > 8 * sms)) break;
     const int64_t parts = (tiles + each - 1) / each;
     if (parts != s) continue;
-    const int64_t cost = (ctas * s + sms - 1) / sms * (each + kFixed) + (s > 1 ? kFixed : 0);
+    const int64_t cost = (ctas * s + sms - 1) / sms * (each + kFixed) + (s > 1 ? kFixed + rows * s / kRowsATile : 0);
     if (best < 0 || cost < best) {
       best = cost;
       c.splits = (int)s;
