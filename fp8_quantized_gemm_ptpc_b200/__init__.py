@@ -194,6 +194,15 @@ def _need(t: torch.Tensor, name: str, dtype, ndim: int):
         raise ValueError(f"{name} must be a contiguous {ndim}-d tensor")
 
 
+def _need_on(index: int, t: torch.Tensor, name: str, dtype, ndim: int):
+    """_need, and the device; one expression where all is well."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype == dtype and t.dim() == ndim and \
+            t.is_contiguous():
+        return
+    _need(t, name, dtype, ndim)
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+
+
 def _need_rows(t: torch.Tensor, name: str) -> int:
     """A bf16 [rows, cols] tensor whose rows are contiguous (a dense tensor or
     a column slice of one); returns the row pitch in elements."""
@@ -350,8 +359,9 @@ def _same_device(device: torch.device, *tensors):
             raise ValueError(f"the tensors are on {t.device} and on {device}")
 
 
-def _fresh(like: torch.Tensor) -> torch.Tensor:
-    return torch.empty_like(like, memory_format=torch.contiguous_format)
+def _fresh(like: torch.Tensor, dtype=torch.bfloat16) -> torch.Tensor:
+    """A dense output of like's shape (half the host time of torch.empty)."""
+    return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def _norm_args(y, residual, pre_weight, post_weight, gate, h_out):
@@ -364,16 +374,16 @@ def _norm_args(y, residual, pre_weight, post_weight, gate, h_out):
         if y.shape != shape:
             raise ValueError("y and residual differ in shape")
     _need(pre_weight, "pre_weight", torch.bfloat16, 1)
-    if len(pre_weight) != C:
+    if pre_weight.shape[0] != C:
         raise ValueError(f"pre_weight must have {C} values")
     if post_weight is not None:
         _need(post_weight, "post_weight", torch.bfloat16, 1)
-        if len(post_weight) != C:
+        if post_weight.shape[0] != C:
             raise ValueError(f"post_weight must have {C} values")
     if gate is not None:
         if isinstance(gate, torch.Tensor) and gate.dim() == 1:
             _need(gate, "gate", torch.bfloat16, 1)
-            if len(gate) != C:
+            if gate.shape[0] != C:
                 raise ValueError(f"gate must have {C} values")
         else:
             ldg = _need_rows(gate, "gate")
@@ -424,18 +434,20 @@ def residual_norm_quantize(y, residual, pre_weight, post_weight=None, gate=None,
     """residual_norm with x as the per-token E4M3 codes and scales that
     scaled_mm reads -> (h bf16 [T, C], Xq uint8 [T, C], x_scale fp32 [T])."""
     h_out, args, ldh = _norm_args(y, residual, pre_weight, post_weight, gate, h_out)
-    shape = residual.shape
     if Xq is None:
-        Xq = residual.new_empty(shape, dtype=torch.uint8)
+        Xq = _fresh(residual, torch.uint8)
     else:
         _need(Xq, "Xq", torch.uint8, 2)
+        if Xq.shape != residual.shape:
+            raise ValueError("Xq and residual differ in shape")
+        _same_device(residual.device, Xq)
     if x_scale is None:
-        x_scale = residual.new_empty(shape[0], dtype=torch.float32)
+        x_scale = residual.new_empty(residual.shape[0], dtype=torch.float32)
     else:
         _need(x_scale, "x_scale", torch.float32, 1)
-    if Xq.shape != shape or len(x_scale) != shape[0]:
-        raise ValueError("Xq or x_scale does not fit residual")
-    _same_device(residual.device, Xq, x_scale)
+        if x_scale.shape[0] != residual.shape[0]:
+            raise ValueError(f"x_scale must have {residual.shape[0]} values")
+        _same_device(residual.device, x_scale)
     _check("ptpc_residual_norm_quantize",
            lib.ptpc_residual_norm_quantize(*args, float(eps), float(residual_scale), _ptr(h_out), ldh, _ptr(Xq),
                                            _ptr(x_scale), _stream(residual.device)))
@@ -745,12 +757,12 @@ def _need_heads(t: torch.Tensor, name: str) -> int:
     return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
-def _need_cache(k_cache, v_cache, k_scale, v_scale):
+def _need_cache(index: int, k_cache, v_cache, k_scale, v_scale):
     """Checks the four tensors of a paged cache; returns (num_blocks, block_size, H, D)."""
-    _need(k_cache, "k_cache", torch.uint8, 4)
-    _need(v_cache, "v_cache", torch.uint8, 4)
-    _need(k_scale, "k_scale", torch.float32, 3)
-    _need(v_scale, "v_scale", torch.float32, 3)
+    _need_on(index, k_cache, "k_cache", torch.uint8, 4)
+    _need_on(index, v_cache, "v_cache", torch.uint8, 4)
+    _need_on(index, k_scale, "k_scale", torch.float32, 3)
+    _need_on(index, v_scale, "v_scale", torch.float32, 3)
     shape, scales = k_cache.shape, k_scale.shape
     if v_cache.shape != shape or scales != shape[:3] or v_scale.shape != scales:
         raise ValueError("shape mismatch")
@@ -771,12 +783,15 @@ def rope_kv_cache_append(q, k, v, cos_sin, positions, slots, k_cache, v_cache, k
     interleaved.  q_out may be q.  Of a token whose position is outside the
     table nothing is written (a fresh q_out is then undefined there)."""
     ldq, ldk, ldv = _need_heads(q, "q"), _need_heads(k, "k"), _need_heads(v, "v")
-    _need(cos_sin, "cos_sin", torch.float32, 2)
-    _need(positions, "positions", torch.int64, 1)
-    _need(slots, "slots", torch.int64, 1)
-    nb, bs, Hkv, D = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    device = q.device
+    index = device.index
+    _need_on(index, cos_sin, "cos_sin", torch.float32, 2)
+    _need_on(index, positions, "positions", torch.int64, 1)
+    _need_on(index, slots, "slots", torch.int64, 1)
+    nb, bs, Hkv, D = _need_cache(index, k_cache, v_cache, k_scale, v_scale)
     T, Hq, Dq = q.shape
-    if Dq != D or k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D) or len(positions) != T or len(slots) != T:
+    kv = (T, Hkv, D)
+    if Dq != D or k.shape != kv or v.shape != kv or positions.shape[0] != T or slots.shape[0] != T:
         raise ValueError("shape mismatch")
     ldo = Hq * D
     if q_out is None:
@@ -785,13 +800,14 @@ def rope_kv_cache_append(q, k, v, cos_sin, positions, slots, k_cache, v_cache, k
         ldo = _need_heads(q_out, "q_out")
         if q_out.shape != q.shape:
             raise ValueError("q_out and q differ in shape")
-    _same_device(q.device, k, v, cos_sin, positions, slots, k_cache, v_cache, k_scale, v_scale, q_out)
+    _same_device(device, k, v, q_out)
     rows, turned = cos_sin.shape
     _check("ptpc_rope_kv_cache_append",
-           lib.ptpc_rope_kv_cache_append(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(cos_sin), rows,
-                                         turned, int(bool(interleaved)), _ptr(positions), _ptr(slots), T, Hq, Hkv, D,
-                                         bs, nb, _ptr(q_out), ldo, _ptr(k_cache), _ptr(v_cache),
-                                         _ptr(k_scale), _ptr(v_scale), _stream(q.device)))
+           lib.ptpc_rope_kv_cache_append(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, cos_sin.data_ptr(),
+                                         rows, turned, 1 if interleaved else 0, positions.data_ptr(),
+                                         slots.data_ptr(), T, Hq, Hkv, D, bs, nb, q_out.data_ptr(), ldo,
+                                         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                         v_scale.data_ptr(), _stream(device)))
     return q_out
 
 
@@ -846,32 +862,34 @@ def chunk_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, context
     fresh out is undefined there).  In a graph capture without ``ws`` the call
     gets a workspace of its own from the capture's pool."""
     ldq = _need_heads(q, "q")
-    nb, bs, Hkv, D = _need_cache(k_cache, v_cache, k_scale, v_scale)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(context_lens, "context_lens", torch.int32, 1)
-    _need(cu_q, "cu_q", torch.int32, 1)
+    device = q.device
+    index = device.index
+    nb, bs, Hkv, D = _need_cache(index, k_cache, v_cache, k_scale, v_scale)
+    _need_on(index, block_tables, "block_tables", torch.int32, 2)
+    _need_on(index, context_lens, "context_lens", torch.int32, 1)
+    _need_on(index, cu_q, "cu_q", torch.int32, 1)
     total, Hq, Dq = q.shape
-    B = len(context_lens)
+    B = context_lens.shape[0]
     tables, table_blocks = block_tables.shape
-    if Dq != D or Hq % max(Hkv, 1) or tables != B or len(cu_q) != B + 1:
+    if Dq != D or Hq % max(Hkv, 1) or tables != B or cu_q.shape[0] != B + 1:
         raise ValueError("shape mismatch")
     if out is None:
         out = _fresh(q)
     else:
-        _need(out, "out", torch.bfloat16, 3)
+        _need_on(index, out, "out", torch.bfloat16, 3)
         if out.shape != q.shape:
             raise ValueError("out and q differ in shape")
-    _same_device(q.device, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, cu_q, out)
     need = int(lib.ptpc_chunk_attention_workspace_size(total, B, Hq, Hkv, D, max_q, max_context))
     if ws is not None:
         ws.ensure(need)
+        _same_device(device, ws.buf)
     elif torch.cuda.is_current_stream_capturing():
-        ws = Workspace.status_only(need, q.device)
+        ws = Workspace.status_only(need, device)
     else:
-        ws = default_workspace(need, q.device)
+        ws = default_workspace(need, device)
     _check("ptpc_chunk_attention",
-           lib.ptpc_chunk_attention(_ptr(q), ldq, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                    _ptr(block_tables), _ptr(context_lens), _ptr(cu_q), total, B, max_q, Hq, Hkv, D,
-                                    bs, nb, table_blocks, max_context, float(softmax_scale), _ptr(out), ws.ptr(),
-                                    ws.nbytes, _stream(q.device)))
+           lib.ptpc_chunk_attention(q.data_ptr(), ldq, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                    v_scale.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+                                    cu_q.data_ptr(), total, B, max_q, Hq, Hkv, D, bs, nb, table_blocks, max_context,
+                                    float(softmax_scale), out.data_ptr(), ws.ptr(), ws.nbytes, _stream(device)))
     return out

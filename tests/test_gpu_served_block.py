@@ -191,3 +191,56 @@ def test_captured_steps_replay_what_runs_eagerly(ptpc):
         want = eager.step(ptpc, new, *batch([1] * B, [x + 1 + i for x in m]), 1, 300)
         torch.cuda.current_stream().wait_stream(side)
         assert all(torch.equal(a, b) for a, b in zip(outs[i % 2], want))
+
+
+def test_wrappers_refuse_what_does_not_fit(ptpc):
+    """Before anything is launched: other types, shapes, pitches and devices."""
+    T, nb = 6, 4
+    x, w = stream(T, 30), torch.ones(C, dtype=torch.bfloat16, device="cuda")
+    fine = dict(y=x, residual=x, pre_weight=w, post_weight=w, gate=w)
+    for call in (ptpc.residual_norm, ptpc.residual_norm_quantize):
+        for name, bad, error in (
+                ("y", x[:, :-16], ValueError), ("y", x.float(), TypeError), ("y", x.t(), ValueError),
+                ("residual", x.cpu(), TypeError), ("residual", x[0], ValueError), ("pre_weight", w[:-16], ValueError),
+                ("pre_weight", w.cpu(), TypeError), ("post_weight", w.float(), TypeError), ("gate", x[:-1], ValueError),
+                ("gate", w[:16], ValueError), ("h_out", x[:, :-16], ValueError), ("y", None, ptpc.PtpcError),
+                ("eps", 0.0, ptpc.PtpcError), ("residual_scale", math.inf, ptpc.PtpcError)):
+            with pytest.raises(error):
+                call(**{**fine, name: bad})
+    with pytest.raises(ValueError):
+        ptpc.residual_norm(x, x, w, out=torch.zeros(T, 2 * C, dtype=torch.bfloat16, device="cuda")[:, :C])
+    with pytest.raises(ValueError):
+        ptpc.residual_norm_quantize(x, x, w, Xq=torch.zeros(T, C + 16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        ptpc.residual_norm_quantize(x, x, w, x_scale=torch.zeros(T + 1, device="cuda"))
+
+    q = stream(T, 31).view(T, Hq, D)
+    k = q[:, :Hkv]
+    cache = [torch.zeros(nb, BS, Hkv, D, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.ones(nb, BS, Hkv, device="cuda") for _ in range(2)]
+    at = torch.arange(T, device="cuda")
+    table = torch.zeros(16, D, device="cuda")
+    fine = dict(q=q, k=k, v=k, cos_sin=table, positions=at, slots=at, k_cache=cache[0], v_cache=cache[1],
+                k_scale=scales[0], v_scale=scales[1])
+    for name, bad, error in (
+            ("q", q.float(), TypeError), ("q", q.transpose(0, 1), ValueError), ("k", q, ValueError),
+            ("v", k[:-1], ValueError), ("cos_sin", table.double(), TypeError), ("cos_sin", table[:, :24].contiguous(), ptpc.PtpcError),
+            ("positions", at.int(), TypeError), ("slots", at[:-1], ValueError), ("slots", at.cpu(), TypeError),
+            ("k_scale", scales[0][:, :8], ValueError), ("v_cache", cache[1][:2], ValueError), ("q_out", k, ValueError)):
+        with pytest.raises(error):
+            ptpc.rope_kv_cache_append(**{**fine, name: bad})
+
+    i32 = dict(dtype=torch.int32, device="cuda")
+    fine = dict(q=q, k_cache=cache[0], v_cache=cache[1], k_scale=scales[0], v_scale=scales[1],
+                block_tables=torch.zeros(2, 4, **i32), context_lens=torch.ones(2, **i32), cu_q=torch.zeros(3, **i32),
+                max_q=4, max_context=64, softmax_scale=0.1)
+    for name, bad, error in (
+            ("q", q[:, :3].contiguous(), ValueError), ("q", q[..., :64].contiguous(), ValueError),
+            ("block_tables", torch.zeros(3, 4, **i32), ValueError), ("context_lens", at[:2], TypeError),
+            ("cu_q", torch.zeros(2, **i32), ValueError), ("cu_q", torch.zeros(3, dtype=torch.int32), TypeError),
+            ("max_q", -1, ptpc.PtpcError), ("softmax_scale", 0.0, ptpc.PtpcError), ("out", q[:-1], ValueError),
+            ("ws", ptpc.Workspace(256, "cpu"), ValueError)):
+        with pytest.raises(error):
+            ptpc.chunk_attention(**{**fine, name: bad})
+    for c in cache:
+        assert int(c.sum()) == 0
