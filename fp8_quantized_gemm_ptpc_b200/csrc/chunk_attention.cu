@@ -53,10 +53,11 @@
 // Measured and dropped: scores of 128 columns (the MMAs of both streams then
 // collide, and shared memory answers the converters late), one S buffer and two
 // of P' a stream, four softmax warpgroups, the next scores' loads ahead of P'
-// (all slower); converter code apart for whole tiles (no gain); a polynomial for
-// one exponential in sixteen (3% faster, not kept for its special cases), for more
-// (slower); L2 prefetches two tiles ahead (8% faster for single tokens, 2% slower
-// for chunks).
+// (all slower); converter code apart for whole tiles, a polynomial for one
+// exponential in sixteen (no gain), for more (slower); L2 prefetches two tiles
+// ahead (8% faster for single tokens, 2% slower for chunks) or by the spare
+// warps (6% faster, drafts 2% slower); with few rows a third stage of V, the
+// kernel as a programmatic dependent, tensor memory ahead of the search (no gain).
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
