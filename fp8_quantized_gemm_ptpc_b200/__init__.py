@@ -341,10 +341,15 @@ def _on_device(fn):
     @functools.wraps(fn)
     def call(*args, **kwargs):
         index = -1
-        for a in args or kwargs.values():
+        for a in args:
             if isinstance(a, torch.Tensor):
                 index = a.get_device()
                 break
+        else:
+            for a in kwargs.values():
+                if isinstance(a, torch.Tensor):
+                    index = a.get_device()
+                    break
         if index < 0 or index == _current_device():
             return fn(*args, **kwargs)
         with torch.cuda.device(index):

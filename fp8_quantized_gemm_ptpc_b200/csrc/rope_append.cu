@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
     if (active && h < heads) raw[i] = ld_stream(from + (int64_t)(h - (is_q ? 0 : is_k ? p.Hq : p.Hq + p.Hkv)) * L + lane);
   }
   // the angles of this lane's pairs: 8 (one half of each pair is here), or 4
-  // when interleaved (both halves are); cosine 1 and sine 0 where nothing turns
+  // when interleaved (both halves are)
   constexpr int A = INTERLEAVED ? 4 : 8;
   const int half = p.rot / 2;
   const bool turns = active && e0 < p.rot;
