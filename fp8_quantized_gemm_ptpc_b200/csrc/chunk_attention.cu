@@ -16,15 +16,23 @@
 // kref is a power of two at least the largest key scale; the product is formed
 // as code * hi + code * lo with the ratio split in two f16, so K' is rounded
 // once.  vref is 2^-6 of such a power for the value scales: V' reaches 448 *
-// 64, near f16's largest value, so that the ratio keeps f16's 11 bits down to
-// 2^-20 of the largest scale.  A key's error is 2^-12 of its value, spread over
-// D products; a value's at most 2^-11.
+// 64, near f16's largest value.  An error is at most 2^-11 of the key or value
+// itself.
+// Scales go by a common reference only where they lie within 2^6 of the largest
+// of the 32 (kCaSpread).  Otherwise one position would take f16's range, for P'
+// as for K' and V', from the others: a zero vector, which has scale 1, or a
+// large one that a row does not even see.  Such 32 positions keep their codes as
+// they are (V's times 64) and have factors of their own, which the softmax takes
+// from COLS, unit by unit of 64 positions and a good deal slower (apart_unit); a
+// zero value weighs in the sum alone.  Keeping that code out of the loop that
+// other units take matters: in one body with it they were 3.5% slower, and now
+// 1% (2048 tokens on 30,720; the converters' tests of the scales, most of it).
 // Warps 16 and 17 (a stream each) issue S = Q K'^T (kind::f16, q as f16 after a
 // power-of-two scale a row, exact) and O += P' V' with P' from tensor memory.
 // Warps 0-3 and 4-7 (a stream each, a thread a row) do the softmax in base 2.
 // With t = S * kref * qscale * log2 e, a weight is P' = 2^(t + log2 vref - r):
 // the reference r follows the largest t + log2 vref, so the f16 P' stays near
-// 1 however the value scales spread, and the sum of 2^(t - r) is that of P' /
+// 1 whatever the values' size, and the sum of 2^(t - r) is that of P' /
 // vref.  r moves (and O, in tensor memory, is rescaled) only when the weights
 // of 64 positions, taken with the r of before, sum to 2^15 or more, which also
 // keeps each below f16's largest value: the common case needs no maximum at
@@ -87,12 +95,15 @@ constexpr uint32_t kStatusTimeoutChunk = 1u << 4;
 constexpr float kCaMost = 32768.0f;   // r is looked at again when a row's weights of 64 positions reach this sum,
 constexpr float kCaLazy = 8.0f;       // and moves where the largest exceeds it by this (64 * 2^8 < kCaMost)
 constexpr int kCaMaxSplits = 64;
+constexpr uint32_t kCaSpread = 6u << 23;    // scales share a reference within 2^6 of the largest (float bits),
+constexpr uint32_t kCaLeast = 53u << 23;    // and from 2^-74 on
+constexpr float kCaNoValue = -88.0f;        // what log2 of a value's scale counts as in r, at least
 
 // What the softmax needs of a tile: for each of its two halves of 64 positions
 // and the 32-position parts of a half
 struct TileMeta {
   struct Half {
-    float kref[2], lv[2];                   // lv = log2 vref
+    float kref[2], lv[2];                   // lv = log2 vref; NaN: a position has factors of its own (CaSmem::COLS)
     float inv_vref[2];
     uint32_t valid[2];                      // bit i: the position is in the cache
   } half[2];
@@ -127,7 +138,8 @@ struct CaSmem {
   static constexpr int V = K + kCaStages * kOperand;        // [stage]
   static constexpr int META = V + kCaStages * kOperand;
   static constexpr int ML = META + kCaMeta * (int)sizeof(TileMeta);  // [row]: r and l of stream 1 when joined
-  static constexpr int BARS = ML + kCaRows * 8;
+  static constexpr int COLS = ML + kCaRows * 8;             // [tile of kCaMeta][position]: what kref and lv are for it alone
+  static constexpr int BARS = COLS + kCaMeta * kCaTile * 8;
   static constexpr int kBars = 4 * kCaStages + 3 * 4 + 3;
   static constexpr int BYTES = 1024 + BARS + kBars * 8 + 16;
 };
@@ -236,6 +248,17 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, u
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_32x32b_x4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -330,6 +353,14 @@ __device__ __forceinline__ int piece_off(int r, int c) {
 // be a generic one).
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t at, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(a), "f"(b) : "memory");
+}
+__device__ __forceinline__ float2 lds64(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
 }
 __device__ __forceinline__ void sts32(uint32_t at, uint32_t a) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(a) : "memory");
@@ -545,12 +576,12 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     auto load_scale = [&](const float *scales, int slot) {
       return ld_scale(scales + (int64_t)max(slot, 0) * p.Hkv + kvh);
     };
-    // bits of a positive finite scale, 0 otherwise
-    auto usable = [](float s) -> uint32_t { return s > 0.0f && s < INFINITY ? __float_as_uint(s) : 0u; };
+    // bits of a finite scale's magnitude, 0 otherwise
+    auto usable = [](float s) -> uint32_t { return fabsf(s) < INFINITY ? __float_as_uint(fabsf(s)) : 0u; };
     // The value scale that counts: 0 where there is none.  A zero vector has
-    // scale 1 whatever its neighbours': taken as 0 too, or its 32 positions'
-    // weights would crowd out the others'.  Only a scale of exactly 1 makes
-    // the warp look (a wait for memory, but a rare one).
+    // scale 1 whatever its neighbours': taken as 0 too, or its weight would
+    // crowd out the others'.  Only a scale of exactly 1 makes the warp look (a
+    // wait for memory, but a rare one).
     auto value_scale = [&](float scale, int slot) -> float {
       const bool one = slot >= 0 && scale == 1.0f;
       if (!__any_sync(0xffffffffu, one)) return slot >= 0 ? scale : 0.0f;
@@ -567,9 +598,11 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     };
     // The reference of 32 scales: a power of two >= the largest usable one,
     // less `below` powers, in [2^-90, 2^120] (1: there is none); as bits.
-    auto reference = [&](float scale, uint32_t below) -> uint32_t {
-      const uint32_t top = __reduce_max_sync(0xffffffffu, usable(scale));
+    // apart: not all of the positions in the cache can go by it.
+    auto reference = [&](float scale, int slot, uint32_t below, bool &apart) -> uint32_t {
+      const uint32_t mine = usable(scale), top = __reduce_max_sync(0xffffffffu, mine);
       const uint32_t up = (top + 0x007FFFFFu) & 0x7F800000u;
+      apart = __any_sync(0xffffffffu, slot >= 0 && (mine < kCaLeast || top - mine > kCaSpread));
       return top != 0 ? min(max(up, 43u << 23) - (below << 23), 247u << 23) : 127u << 23;
     };
     // 2^-x of a power of two 2^x
@@ -622,12 +655,16 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       const float next_ksc = load_scale(p.ks, next), next_vsc = load_scale(p.vs, next);
       const float v_scale = value_scale(vsc, slot);
       const float scale = is_k ? (slot >= 0 ? ksc : 0.0f) : v_scale;
-      const uint32_t vb = reference(v_scale, 6), ref = is_k ? reference(scale, 0) : vb;
+      bool v_apart, k_apart = false;
+      const uint32_t vb = reference(v_scale, slot, 6, v_apart), ref = is_k ? reference(scale, slot, 0, k_apart) : vb;
       const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
       // x' = code * scale / ref, the ratio as a sum of two f16
       const float ratio = scale * inverse(ref);
       const float hi = __half2float(__float2half_rn(ratio));
       uint32_t split2 = f16_pair(hi, ratio - hi);   // of an infinite scale: NaN (K: in its column alone)
+      // scales apart: the codes as they are, V's times 64, exact
+      if (__builtin_expect(is_k ? k_apart : v_apart, 0))
+        split2 = is_k ? f16_pair(1.0f, 0.0f) : f16_pair(scale - scale + copysignf(64.0f, scale), 0.0f);
       uint32_t nan = 0;
       // tiles that some rows see in part: P' = 0 must cancel a value that is
       // not finite, so its vector is zeroed and marked for the rows that see it
@@ -650,11 +687,19 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       }
       ok = wait_free(empty, j);
       if (!ok) break;
+      const float lv = (float)((int)(vb >> 23) - 127);
+      if (is_k) {
+        // each position's own factors, which one with its scale apart goes by
+        // (and the 64 positions that go through the softmax with it)
+        const float kf = k_apart ? scale - scale + scale : __uint_as_float(ref);
+        const float vf = v_apart ? (usable(v_scale) != 0 ? __log2f(fabsf(v_scale)) - 6.0f : -INFINITY) : lv;
+        sts64(smem_u32(sm + S::COLS) + ((j % kCaMeta) * kCaTile + 32 * cw + lane) * 8, kf, vf);
+      }
       if (lane == 0) {
         if (is_k) {
           const uint32_t m = smem_u32(&meta[j % kCaMeta].half[cw >> 1]) + (cw & 1) * 4;
           sts32(m, ref);
-          sts32(m + 8, __float_as_uint((float)((int)(vb >> 23) - 127)));
+          sts32(m + 8, v_apart || k_apart ? 0x7FC00000u : __float_as_uint(lv));
           sts32(m + 16, __float_as_uint(inverse(vb)));
           sts32(m + 24, valid);
         } else if (partial) {
@@ -893,13 +938,88 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         sum[c] = both.x + both.y;
       }
     };
-    auto hand_over = [&](int u) {
-      tmem_st_32x32b_x16(ts + 64 * (u & 1), y[0]);
-      tmem_st_32x32b_x16(ts + 64 * (u & 1) + 16, y[1]);
+    auto give = [&](int u) {
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[2 * stream + (u & 1)]);
+    };
+    auto hand_over = [&](int u) {
+      tmem_st_32x32b_x16(ts + 64 * (u & 1), y[0]);
+      tmem_st_32x32b_x16(ts + 64 * (u & 1) + 16, y[1]);
+      give(u);
+    };
+    // Where the row's reference moves to `high`: l follows here, the factor for
+    // O is returned.  By its root twice: l may reach 2^88 a position, so that
+    // some of it is left where the factor is below fp32's smallest number.
+    auto factor = [&](bool move, float high) -> float {
+      const float root = move && r != -INFINITY ? ex2(0.5f * (r - high)) : 1.0f;
+      if (move) r = high;
+      l = l * root * root;
+      return root * root;
+    };
+    // Whether a position of a unit has factors of its own, and such a unit as a
+    // whole: seldom, so few scores at a time in little code.
+    auto is_apart = [&](int u) -> bool {
+      const uint4 m = lds128(smem_u32(&meta[tile(u) % kCaMeta].half[u & 1]));
+      return !(__uint_as_float(m.z) + __uint_as_float(m.w) < INFINITY);
+    };
+    auto apart_unit = [&](int u) -> bool {
+      constexpr int kFew = 8;
+      const uint4 m = lds128(smem_u32(&meta[tile(u) % kCaMeta].half[u & 1]) + 16);
+      const uint32_t own = smem_u32(sm + S::COLS) + ((tile(u) % kCaMeta) * kCaTile + 64 * (u & 1)) * 8;
+      const int before = sees - ((k.t0 + tile(u)) * kCaTile + 64 * (u & 1));
+      // f(i, score less `from`, log2 of the value's scale) of a few positions
+      auto few = [&](int at, float from, auto f) {
+        uint32_t sc[kFew];
+        tmem_ld_32x32b_x8(ts + 64 * (u & 1) + at, sc);
+        tmem_wait_ld();
+        const uint32_t there = (at & 32 ? m.w : m.z) >> (at & 31);
+        #pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+          const float2 f_own = lds64(own + (at + i) * 8);
+          const float t = fmaf(__uint_as_float(sc[i]), f_own.x * rowfac, -from);
+          f(i, ((there >> i) & 1u) != 0 && at + i < before ? t : -INFINITY, f_own.y);
+        }
+      };
+      float high = -INFINITY;
+      #pragma unroll 1
+      for (int at = 0; at < 64; at += kFew)
+        few(at, 0.0f, [&](int, float t, float v) { high = fmaxf(high, t + fmaxf(v, kCaNoValue)); });
+      const bool move = high > r + kCaLazy;
+      if (__any_sync(0xffffffffu, move)) {
+        const float f = factor(move, high);
+        if (u > 0) {
+          if (!__all_sync(0xffffffffu, bar_wait(&o_done[2 * stream + ((u - 1) & 1)], (uint32_t)((u - 1) >> 1) & 1u)))
+            return false;
+          tc_fence_after();
+          #pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(to + c, o);
+            tmem_wait_ld();
+            #pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st_32x32b_x16(to + c, o);
+          }
+        }
+      }
+      const float rs = r == -INFINITY ? 0.0f : r;
+      #pragma unroll 1
+      for (int at = 0; at < 64; at += kFew) {
+        float w[kFew];
+        few(at, rs, [&](int i, float t, float v) {
+          l += ex2(t);
+          w[i] = ex2(t + v);
+        });
+        uint32_t half[kFew / 2];
+        #pragma unroll
+        for (int i = 0; i < kFew; i += 2) half[i / 2] = f16_pair(w[i], w[i + 1]);
+        // over scores that have been taken: half as many columns
+        tmem_st_32x32b_x4(ts + 64 * (u & 1) + at / 2, half);
+      }
+      give(u);
+      return true;
     };
     if (!__any_sync(0xffffffffu, has_row)) {
       // none of the warp's rows is a token's: their weights are never used
@@ -918,6 +1038,12 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         ok = wait_scores(u);
         if (!ok) break;
         tc_fence_after();
+        if (is_apart(u)) {
+          ok = apart_unit(u);
+          if (!ok) break;
+          ++u;
+          continue;
+        }
         start(u);
         arrive();
         const int before = sees - ((k.t0 + tile(u)) * kCaTile + 64 * (u & 1));   // positions of it that the row sees
@@ -936,9 +1062,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         }
         const bool move = high > r + kCaLazy;
         if (__any_sync(0xffffffffu, move)) {
-          const float f = move && r != -INFINITY ? ex2(r - high) : 1.0f;
-          if (move) r = high;
-          l *= f;
+          const float f = factor(move, high);
           if (u > 0) {
             // O follows, once the product of the unit before is done
             ok = __all_sync(0xffffffffu, bar_wait(&o_done[2 * stream + ((u - 1) & 1)], (uint32_t)((u - 1) >> 1) & 1u));
@@ -1029,9 +1153,10 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         const float2 o = ml1[lrow];
         if (o.y != 0.0f) {   // NaN too
           const float rn = fmaxf(r, o.x);
-          f0 = l == 0.0f ? 0.0f : ex2(r - rn);
-          f1 = ex2(o.x - rn);
-          l = l * f0 + o.y * f1;
+          const float root0 = l == 0.0f ? 0.0f : ex2(0.5f * (r - rn)), root1 = ex2(0.5f * (o.x - rn));
+          f0 = root0 * root0;
+          f1 = root1 * root1;
+          l = l * root0 * root0 + o.y * root1 * root1;
           r = rn;
         }
       }
@@ -1051,6 +1176,12 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
           if (tm.nan[c] & tm.half[c >> 1].valid[c & 1] & causal) l = __uint_as_float(0x7FC00000u);
         }
       }
+      // the row's place again: not kept in registers through the units
+      uint32_t tid;
+      asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+      const int again = (two && stream == 1 ? kCaRows : 0) + (int)(tid & 127), R = k.row0 + again;
+      const bool has_row = again < k.rows;
+      const int tok = R / p.G, head = R - tok * p.G;
       const int64_t oh = (int64_t)(k.first_q + tok) * p.Hq + kvh * p.G + head;
       const int64_t part = oh * p.splits + split;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -1143,8 +1274,8 @@ __global__ void __launch_bounds__(256) chunk_attn_combine_kernel(const ChunkArgs
   float l = 0.0f;
   for (int s = 0; s < p.splits; ++s) {
     if (ml[2 * s + 1] == 0.0f) continue;
-    const float w = ex2(ml[2 * s] - top);
-    l = fmaf(ml[2 * s + 1], w, l);
+    const float root = ex2(0.5f * (ml[2 * s] - top)), w = root * root;
+    l = fmaf(ml[2 * s + 1] * root, root, l);
     const float *a = p.part_acc + (oh * p.splits + s) * D + lane * N;
     #pragma unroll
     for (int i = 0; i < N; i += 2) {

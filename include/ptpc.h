@@ -465,10 +465,15 @@ PTPC_API size_t ptpc_chunk_attention_workspace_size(int64_t total_q, int64_t B, 
  *              0 for a token that sees no position (m < n, or no block in the table).
  *   ws_dev     ptpc_chunk_attention_workspace_size(...) bytes; its first word must be zero
  *              before the first call and is the device status word (ptpc_get_device_status).
- * The products run on the tensor cores in f16 with fp32 accumulation: keys and
- * values enter as code * scale / (a scale of 32 positions), rounded to f16's 11
- * bits, weights as f16, statistics and sums are fp32.  Results do not depend
- * on the other sequences of the call as long as the plan (below) is the same. */
+ * The products run on the tensor cores in f16 with fp32 accumulation: queries
+ * enter over a power of two a row (a value below 2^-14 of its row's largest loses
+ * bits, one below 2^-25 counts as 0), keys and values as code * scale / (a common
+ * scale of 32 positions), rounded to f16's 11 bits, or exactly where the scales of
+ * the 32 are more than 2^6 apart; weights as f16, with a step of 2^-24 of the
+ * largest weighed value's, statistics and sums in fp32.  Value scales below 2^-96
+ * lose bits.  Results do not depend on the other sequences of the call as long as
+ * the plan (below) is the same.  The scales of later tokens among the same 32
+ * positions may change a row's roundings, within these bounds. */
 PTPC_API int ptpc_chunk_attention(const void *q_dev, int64_t ldq, const uint8_t *k_cache_dev,
                                   const uint8_t *v_cache_dev, const float *k_scale_dev, const float *v_scale_dev,
                                   const int32_t *block_tables_dev, const int32_t *context_lens_dev,
