@@ -219,8 +219,9 @@ def _need_rows(t: torch.Tensor, name: str) -> int:
 class Workspace:
     """A zero-filled device buffer for the entry points that take (ws, ws_bytes).
 
-    The library leaves its control words zero after every successful call, so
-    one buffer serves any number of calls that do not overlap on the GPU.  A
+    The library reads nothing of it but the status word at its front that the
+    same call has not written, so one buffer serves any number of calls that do
+    not overlap on the GPU.  A
     workspace belongs to one stream: the buffer is allocated (and zeroed) on
     the stream that is current when it is created or grown, and the caller
     must not use it on two streams at once."""

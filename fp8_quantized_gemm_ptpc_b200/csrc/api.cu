@@ -100,10 +100,6 @@ int run_gemm(const uint8_t *Xq, const float *xs, const uint8_t *Wq_t, const floa
   p.f32_out = f32_out;
   p.status = reinterpret_cast<uint32_t *>(wsp);
   p.pdl = pdl;
-  if (!pdl && !f32_out) {   // a dependent launch has its counters zeroed ahead of the kernel it follows
-    const int s = cuda_status(ptpc::zero_gemm_counters(p.T, p.Ci, p.Co, wsp, ws_bytes, st));
-    if (s != PTPC_OK) return s;
-  }
   return cuda_status(ptpc::launch_scaled_gemm(p, st));
 }
 

@@ -586,8 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // itself in, waits (bounded) until the tile's 2 * tail_split CTAs have all
 // stored theirs, and then finishes 1 / (2 * tail_split) of the tile: the
 // partials added in split order (a fixed order: deterministic), the two
-// scales applied, bf16 stored.  The counters are zeroed before each launch
-// (zero_gemm_counters): other entry points keep data in the same bytes.
+// scales applied, bf16 stored.  The last CTA to finish zeroes the tile's
+// counters, so that a workspace ends a call as it is handed out; a call relies
+// on none of that: the counters are zeroed before each launch, since other
+// entry points keep data in the same bytes.
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -1771,6 +1773,10 @@ cudaError_t launch_scaled_gemm(const GemmProblem &pr, cudaStream_t st) {
     uint8_t *w = reinterpret_cast<uint8_t *>(pr.status);
     gp.tail_count = reinterpret_cast<uint32_t *>(w + kGemmStatusBytes);
     gp.partials = reinterpret_cast<float *>(w + kGemmStatusBytes + kTailCountBytes);
+    if (!pr.pdl) {
+      const cudaError_t e = cudaMemsetAsync(gp.tail_count, 0, kTailCountBytes, st);
+      if (e != cudaSuccess) return e;
+    }
   }
   gp.xs = pr.xs;
   gp.ws = pr.ws;

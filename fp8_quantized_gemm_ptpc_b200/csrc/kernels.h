@@ -58,9 +58,10 @@ struct GemmProblem {
 
 cudaError_t launch_scaled_gemm(const GemmProblem &p, cudaStream_t st);
 
-// Zeroes the split tail's counters where the shape's plan has one; enqueued
-// ahead of launch_scaled_gemm (of the kernel it depends on, with pdl).  The
+// Zeroes the split tail's counters where the shape's plan has one: the
 // workspace may have served another entry point since, whose data lay there.
+// launch_scaled_gemm does so itself, but with pdl, where a fill between the two
+// kernels would undo the early launch: then it is enqueued ahead of the first.
 cudaError_t zero_gemm_counters(int T, int Ci, int Co, uint8_t *ws, size_t ws_bytes, cudaStream_t st);
 
 // CTAs per tile the decode kernel uses for a shape (1: whole tiles; larger:

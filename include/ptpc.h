@@ -39,10 +39,11 @@
  *     returns PTPC_ERR_CUDA.  No C++ exception crosses this boundary.
  *   - Workspace: entry points that take (ws_dev, ws_bytes) need at least
  *     ptpc_workspace_size(op, T, Ci, Co) bytes, zero-filled before its first
- *     use.  Each successful call leaves the workspace's control words zero
- *     again, so a workspace is zero-filled only once.  Entry points may share
- *     one, call behind call; calls that share a workspace must not overlap on
- *     the GPU.
+ *     use.  Only the device status word at its front has to be zero (it keeps
+ *     what a call sets until ptpc_get_device_status reads it): a call writes
+ *     what it reads of the rest, and zeroes its own control words again.  So
+ *     entry points may share a workspace, call behind call; calls that share
+ *     one must not overlap on the GPU.
  *   - Inputs are assumed finite.  Non-finite inputs do not fault but give
  *     unspecified codes.  The GEMM epilogue multiplies in the order
  *     (acc * x_scale) * w_scale in fp32; outputs are specified where that

@@ -84,3 +84,24 @@ def test_split_tail_captured_behind_other_data(ptpc, layer):
         graph.replay()
         assert torch.equal(got, want)
     assert ptpc.device_status(ws) == 0
+
+
+def test_nothing_but_the_status_word_need_be_zero(ptpc, layer):
+    """Every entry point that takes a workspace, with all of it but the first
+    256 bytes holding ones before each call."""
+    x, w = layer
+    chunk, decode = attention(ptpc)
+    wide = x[:, :1024].contiguous()
+    raw = (torch.arange(1024 * 512, device="cuda").view(1024, 512) % 251 / 64 - 1).to(torch.bfloat16)
+    w4 = ptpc.quantize_weights_fmt(raw, "e2m1")
+    calls = [lambda ws: ptpc.linear(x, *w, ws=ws), lambda ws: ptpc.linear(x[:8], *w, ws=ws), chunk, decode,
+             lambda ws: ptpc.scaled_mm(*ptpc.quantize_activations(x), *w, ws=ws),
+             lambda ws: torch.cat([t.flatten().float() for t in ptpc.quantize_weights(raw, ws=ws)]),
+             lambda ws: torch.cat([t.flatten().float() for t in ptpc.quantize_weights_fmt(raw, "e2m1", ws=ws)]),
+             lambda ws: ptpc.linear_fmt(wide, *w4, "e2m1", ws=ws)]
+    want = [c(ptpc.Workspace(256, "cuda")) for c in calls]
+    ws = ptpc.Workspace(ptpc.workspace_size(ptpc.OP_LINEAR, T, CI, CO), "cuda")
+    for i, c in enumerate(calls):
+        ws.buf[256:] = 255
+        assert torch.equal(c(ws), want[i]), i
+        assert ptpc.device_status(ws) == 0
