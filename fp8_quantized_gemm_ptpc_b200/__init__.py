@@ -866,7 +866,9 @@ def chunk_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, context
     the cache already; block_tables int32 [B, max_blocks].  A token sees the
     positions up to its own.  Rows of no sequence are left as they were (a
     fresh out is undefined there).  In a graph capture without ``ws`` the call
-    gets a workspace of its own from the capture's pool."""
+    gets a workspace of its own from the capture's pool, whose status word
+    nobody can read: whether a bounded wait ran out in a replay shows there by
+    rows of NaN, and in ``device_status`` where ``ws`` is given."""
     ldq = _need_heads(q, "q")
     device = q.device
     index = device.index

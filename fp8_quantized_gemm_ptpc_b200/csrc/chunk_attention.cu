@@ -45,7 +45,7 @@
 //
 // With few rows the context is split over CTAs whose partial results a second
 // kernel joins (plan_chunk).  Every wait is bounded; a timeout sets a bit in
-// the status word at the front of the workspace.
+// the status word at the front of the workspace, and the rows are NaN.
 //
 // What bounds it (B200, heads of 128).  64 positions of both streams take about
 // 1,900 cycles of an SM, in which the products need 620 (the MMAs of 64 columns
@@ -1128,7 +1128,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
     ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutChunk);
     tc_fence_after();
-    if (!ok) l = 0.0f;
+    if (!ok) l = __uint_as_float(0x7FC00000u);   // a wait ran out: NaN, not a part of the sum
     float f0 = l == 0.0f ? 0.0f : 1.0f;   // factor of this stream's O
     float f1 = 0.0f;                      // factor of the other stream's, when the two are joined
     float *joined = reinterpret_cast<float *>(sm + S::K);   // [D][128], in the K ring

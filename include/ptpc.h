@@ -466,6 +466,7 @@ PTPC_API size_t ptpc_chunk_attention_workspace_size(int64_t total_q, int64_t B, 
  *              0 for a token that sees no position (m < n, or no block in the table).
  *   ws_dev     ptpc_chunk_attention_workspace_size(...) bytes; its first word must be zero
  *              before the first call and is the device status word (ptpc_get_device_status).
+ *              Rows for which a bounded wait ran out are NaN.
  * The products run on the tensor cores in f16 with fp32 accumulation: queries
  * enter over a power of two a row (a value below 2^-14 of its row's largest loses
  * bits, one below 2^-25 counts as 0), keys and values as code * scale / (a common
