@@ -55,9 +55,13 @@
 // 3,100 cycles for 128 positions.  A CTA's start and end cost about 17,000
 // cycles (its places 1,200, the first codes and q 7,000, the first scores, its
 // last product and output 6,500, the next CTA's launch 2,500), which is why a
-// context is split only where SMs would idle.  With 64 + 8 heads, 2048 tokens on
-// 30,720 more take 1.96 ms, 0.66 of the measured bf16 rate; with 32 + 8, eight
-// prompts of 300 to 4000 tokens 539 us, 0.48.
+// context is split only where SMs would idle.  Heads of 64 take the same 1,900
+// cycles for half the products.  With 64 + 8 heads, 2048 tokens on 30,720 more
+// take 2.01 ms (0.64 of the measured bf16 rate) a few calls at a time and 2.29 ms
+// (0.56) one behind the other, where the board's power limit holds the clock at
+// 1.5 GHz; with 32 + 8, eight prompts of 300 to 4000 tokens 566 and 595 us (0.46,
+// 0.43; 1.63 GHz).  A step of single tokens is decode_attention's: 32 on 4096
+// positions, 64 + 8 heads, 134 us here and 54 there.
 // Measured and dropped: scores of 128 columns (the MMAs of both streams then
 // collide, and shared memory answers the converters late), one S buffer and two
 // of P' a stream, four softmax warpgroups, the next scores' loads ahead of P'
@@ -1301,11 +1305,12 @@ struct ChunkPlan {
 // pays for the second kernel and its partial results (kRowsATile rows a part
 // take it about a tile's time).  The launch has room for the most row tiles that
 // the bounds allow; the waves are counted for the middle between those and the
-// fewest.  Measured over 26 shapes (geometric means): 43.6 us, with kFixed 6,
-// parts of four tiles or more and the most row tiles 48.3; the middle alone took
-// 67 tokens on 57,435 positions and 64 on 41,014, 32 + 2 heads of 64, from 137 to
-// 121 us; the fewest would put a sequence of one row tile more into a second wave
-// (72 -> 92 us).  One sequence of 5 tokens on 4096 positions: 22.5 us.
+// fewest, which would put a sequence of one row tile more into a second wave (72
+// -> 92 us).  Over 26 shapes, called one behind the other (geometric means): 52.1
+// us, never split 71.1, each shape's best split 49.4; the farthest from its best
+// is three sequences of 43 to 248 tokens on 10,133 to 15,681 positions, 24 + 3
+// heads: 108.4 us in 3 parts, 86.9 in 4, since every part is priced by
+// max_context and by tiles that a shorter sequence does not have.
 ChunkPlan plan_chunk(int64_t total_q, int64_t B, int Hkv, int G, int64_t max_q, int64_t max_context) {
   constexpr int64_t kFixed = 3, kRowsATile = 12000;
   ChunkPlan c;

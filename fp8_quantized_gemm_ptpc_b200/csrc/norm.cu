@@ -19,11 +19,12 @@
 // What keeps it from the floor is issue: 28 instructions a value (a CTA a row 34),
 // a fifth of them the row's reductions and scale in every thread; hence packed
 // fp32 arithmetic and, with many rows, factors kept in shared memory.
-// Measured: 8192 tokens of 8192 columns with both norms, a channel gate and
-// codes 92.5 us (5.1 TB/s, 0.77 of the copy rate; a CTA a row 101), 4000 of
+// Measured in a graph: 8192 tokens of 8192 columns with both norms, a channel gate
+// and codes 92.5 us (5.1 TB/s, 0.77 of the copy rate; a CTA a row 101; repeated
+// calls on changing rows 96.7, 0.74), 4000 of
 // 16384 101 (136), 8192 of 4096 without the norm behind 42.7 (44.8), 3001 of
-// 5136 with a token gate and bf16 out 31.3, 2048 of 4096 10.5 (in L2), one token
-// of 8192 2.7.
+// 5136 with a token gate and bf16 out 31.3 (34.6), 2048 of 4096 10.5 (in L2), one
+// token of 8192 2.7.
 // Copies of the rows ahead into shared memory (cp.async, two or three stages)
 // were slower: 120 to 140 us on the first of these.
 #include <algorithm>

@@ -16,9 +16,9 @@
 // pairs by a shuffle.  A group of lanes takes N heads of one token: N = 4 where
 // there are tokens enough (four loads in flight a lane, and the token's angles,
 // 64 bytes a lane, read once for the four), N = 1 otherwise.  Groups fill the
-// CTAs one behind the other, whatever the number of heads.  Measured: 8192
-// tokens of 64 + 16 heads of 128 62.9 us (5.2 TB/s, 0.78 of the copy rate; N = 2
-// 75.9, N = 5 63.5), of 32 + 16 heads 40.4; 3001 of 12 + 24 heads of 64, half
+// CTAs one behind the other, whatever the number of heads.  Measured in a graph:
+// 8192 tokens of 64 + 16 heads of 128 62.9 us (5.2 TB/s, 0.78 of the copy rate; N =
+// 2 75.9, N = 5 63.5; repeated calls 65.5, 0.75), of 32 + 16 heads 40.4; 3001 of 12 + 24 heads of 64, half
 // turned, 8.1; 32 tokens 2.6.  Issue is next: two cycles of three.
 #include <cstdint>
 #include <cuda_runtime.h>

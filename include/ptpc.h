@@ -445,7 +445,9 @@ PTPC_API size_t ptpc_chunk_attention_workspace_size(int64_t total_q, int64_t B, 
                                                     int64_t max_q, int64_t max_context);
 
 /* Causal attention of each sequence's newest tokens over the FP8 cache (a
- * chunk of a prompt, a whole prompt, drafted tokens, or one token): sequence b
+ * chunk of a prompt, a whole prompt, drafted tokens, or one token beside such;
+ * a step of single tokens alone is faster and a little more exact through
+ * ptpc_decode_attention where Hq / Hkv <= 16): sequence b
  * has n = cu_q[b+1] - cu_q[b] new tokens, the last of its context of
  * context_lens[b] = m positions, all of them in the cache already
  * (ptpc_rope_kv_cache_append).  Token i of them sees positions 0 .. m - n + i.
