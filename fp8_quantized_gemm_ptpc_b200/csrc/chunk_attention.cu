@@ -24,7 +24,8 @@
 // large one that a row does not even see.  Such 32 positions keep their codes as
 // they are (V's times 64) and have factors of their own, which the softmax takes
 // from COLS, unit by unit of 64 positions and a good deal slower (apart_unit); a
-// zero value weighs in the sum alone.  Keeping that code out of the loop that
+// zero value weighs in the sum alone.  Where all are such, 2048 tokens on 30,720
+// take 5.4 ms, with a zero vector every 512 positions 2.9.  Keeping that code out of the loop that
 // other units take matters: in one body with it they were 3.5% slower, and now
 // 1% (2048 tokens on 30,720; the converters' tests of the scales, most of it).
 // Warps 16 and 17 (a stream each) issue S = Q K'^T (kind::f16, q as f16 after a

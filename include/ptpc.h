@@ -477,7 +477,8 @@ PTPC_API size_t ptpc_chunk_attention_workspace_size(int64_t total_q, int64_t B, 
  * largest weighed value's, statistics and sums in fp32.  Value scales below 2^-96
  * lose bits.  Results do not depend on the other sequences of the call as long as
  * the plan (below) is the same.  The scales of later tokens among the same 32
- * positions may change a row's roundings, within these bounds. */
+ * positions may change a row's roundings, within these bounds.  Positions with
+ * scales that far apart (a zero vector has scale 1) take two to three times as long. */
 PTPC_API int ptpc_chunk_attention(const void *q_dev, int64_t ldq, const uint8_t *k_cache_dev,
                                   const uint8_t *v_cache_dev, const float *k_scale_dev, const float *v_scale_dev,
                                   const int32_t *block_tables_dev, const int32_t *context_lens_dev,

@@ -173,13 +173,11 @@ def test_no_value_at_all(ptpc, shape):
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
 @pytest.mark.parametrize("apart", [7, 8, 20, 24, 30, 60])
 def test_value_scales_far_apart(ptpc, apart, shape):
-    """One large vector in 32 (hardly weighed: as likely as the others, but
-    2^-apart of the weight that the others' sum needs is noise for it), and
-    large ones among the hidden positions."""
+    """One vector in 32 is 2^apart times the others and scores as much lower, so
+    that large and small ones count alike in the outputs."""
     c = Cache(**shape, seed=4)
     big = c.at(*[(i, i + 1) for i in range(5, c.m, 32)])
     c.vs[big] *= 2.0 ** apart
-    # the large vectors score so low that small and large ones count alike
     c.score(big, -apart * math.log(2.0))
     c.check(ptpc)
 
