@@ -102,6 +102,7 @@ constexpr float kCaLazy = 8.0f;       // and moves where the largest exceeds it 
 constexpr int kCaMaxSplits = 64;
 constexpr uint32_t kCaSpread = 6u << 23;    // scales share a reference within 2^6 of the largest (float bits),
 constexpr uint32_t kCaLeast = 53u << 23;    // and from 2^-74 on
+constexpr float kCaNear = -100.0f;          // 2^this and sums times it are normal numbers
 constexpr float kCaNoValue = -88.0f;        // what log2 of a value's scale counts as in r, at least
 
 // What the softmax needs of a tile: for each of its two halves of 64 positions
@@ -153,6 +154,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// l 2^by, by <= 0.  A sum l may reach 2^88 a position: some of it is left where
+// the factor itself is below fp32's smallest number.
+__device__ __forceinline__ float times_2to(float l, float by) {
+  return by > kCaNear ? l * ex2(by) : l * ex2(0.5f * by) * ex2(0.5f * by);
 }
 
 __device__ __forceinline__ void ex2_in_order(float &x) { asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(x)); }
@@ -955,13 +962,12 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
       give(u);
     };
     // Where the row's reference moves to `high`: l follows here, the factor for
-    // O is returned.  By its root twice: l may reach 2^88 a position, so that
-    // some of it is left where the factor is below fp32's smallest number.
+    // O is returned.
     auto factor = [&](bool move, float high) -> float {
-      const float root = move && r != -INFINITY ? ex2(0.5f * (r - high)) : 1.0f;
+      const float by = move && r != -INFINITY ? r - high : 0.0f;
       if (move) r = high;
-      l = l * root * root;
-      return root * root;
+      l = times_2to(l, by);
+      return ex2(by);
     };
     // Whether a position of a unit has factors of its own, and such a unit as a
     // whole: seldom, so few scores at a time in little code.
@@ -1158,10 +1164,10 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attn_kernel(const ChunkAr
         const float2 o = ml1[lrow];
         if (o.y != 0.0f) {   // NaN too
           const float rn = fmaxf(r, o.x);
-          const float root0 = l == 0.0f ? 0.0f : ex2(0.5f * (r - rn)), root1 = ex2(0.5f * (o.x - rn));
-          f0 = root0 * root0;
-          f1 = root1 * root1;
-          l = l * root0 * root0 + o.y * root1 * root1;
+          f0 = l == 0.0f ? 0.0f : ex2(r - rn);
+          f1 = ex2(o.x - rn);
+          l = l == 0.0f ? times_2to(o.y, o.x - rn) : fminf(r, o.x) - rn > kCaNear
+              ? l * f0 + o.y * f1 : times_2to(l, r - rn) + times_2to(o.y, o.x - rn);
           r = rn;
         }
       }
@@ -1279,8 +1285,8 @@ __global__ void __launch_bounds__(256) chunk_attn_combine_kernel(const ChunkArgs
   float l = 0.0f;
   for (int s = 0; s < p.splits; ++s) {
     if (ml[2 * s + 1] == 0.0f) continue;
-    const float root = ex2(0.5f * (ml[2 * s] - top)), w = root * root;
-    l = fmaf(ml[2 * s + 1] * root, root, l);
+    const float w = ex2(ml[2 * s] - top);
+    l = ml[2 * s] - top > kCaNear ? fmaf(ml[2 * s + 1], w, l) : l + times_2to(ml[2 * s + 1], ml[2 * s] - top);
     const float *a = p.part_acc + (oh * p.splits + s) * D + lane * N;
     #pragma unroll
     for (int i = 0; i < N; i += 2) {
