@@ -474,10 +474,11 @@ PTPC_API size_t ptpc_chunk_attention_workspace_size(int64_t total_q, int64_t B, 
  * bits, one below 2^-25 counts as 0), keys and values as code * scale / (a common
  * scale of 32 positions), rounded to f16's 11 bits, or exactly where the scales of
  * the 32 are more than 2^6 apart; weights as f16, with a step of 2^-24 of the
- * largest weight times value scale of the row, statistics and sums in fp32.  Value scales below 2^-96
- * lose bits, and weights below 2^-88 of a zero value's.  Results do not depend on the other sequences of the call as long as
- * the plan (below) is the same.  The scales of later tokens among the same 32
- * positions may change a row's roundings, within these bounds.  Positions with
+ * largest weight times value scale of the row, statistics and sums in fp32.  Value
+ * scales below 2^-96 lose bits, and weights below 2^-88 of a zero value's.
+ * Results do not depend on the other sequences of the call as long as the plan
+ * (below) is the same.  The scales of later tokens among the same 32 positions
+ * may change a row's roundings, within these bounds.  Positions with
  * scales that far apart (a zero vector has scale 1) take two to three times as long. */
 PTPC_API int ptpc_chunk_attention(const void *q_dev, int64_t ldq, const uint8_t *k_cache_dev,
                                   const uint8_t *v_cache_dev, const float *k_scale_dev, const float *v_scale_dev,
